@@ -238,7 +238,7 @@ def _framework(st):
         w = st["w"] if c["weighted"] else None
         return L.swiglu_ckpt_bwd(st["q"], st["s"], st["dh"], topk_w=w, inv=st["inv"], out=st["out"])
     if op == "route_bwd":
-        return L.route_bwd(st["x"], st["idx"], st["w"], st["dw"], st["offsets"], st["perm_src"], st["perm_k"])
+        return L.route_bwd(st["x"], st["w"], st["dw"], st["offsets"], st["perm_src"], st["perm_k"])
     if op == "wgrad":
         return L.expert_wgrad(st["dy"], st["a"], st["offsets"], dtype=TYPES[c["src"]])
     return L.expert_product(st["a"], st["w"], st["offsets"], transposed=op == "product_dgrad")
