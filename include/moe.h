@@ -93,7 +93,8 @@ enum { MOE_LOC_HBM = 0, MOE_LOC_HOST_PINNED = 1 };
 enum {
   MOE_DEV_BAD_EXPERT = 1, /* a top-k index outside [0, E) reached moe_permute */
   MOE_DEV_NO_SLOT = 2,    /* a pair was routed to an expert with no registered weights (pair dropped) */
-  MOE_DEV_TIMEOUT = 4     /* a bounded wait inside a kernel gave up (~2 s) */
+  MOE_DEV_TIMEOUT = 4,    /* a bounded wait inside a kernel gave up (~2 s) */
+  MOE_DEV_BAD_INDEX = 8   /* a training call met an inv, perm or offsets entry outside its array (entry ignored) */
 };
 
 typedef struct {
@@ -315,6 +316,119 @@ moe_status_t moe_slots_set_policy(moe_slots_t* slots, int policy);
  *   hist [E] counts (host), hot [n_hot] out (host), listed best first. */
 moe_status_t moe_plan_hot_set(const int64_t* hist, int E, int n_hot, int32_t* hot);
 
+/* ---- training --------------------------------------------------------
+ * The pieces of one training step of the layer: tokens to expert order and
+ * back, the experts' activation with 8-bit checkpoints, the experts' products,
+ * and the gradient of each. Pair i = t*K + k; inv[i] (moe_permute) is its row
+ * in expert order, in [0, T*K), or negative for a dropped pair, which takes no
+ * part: its token's sum leaves it out, its weight's gradient is 0, and rows
+ * behind the last kept pair are neither read nor written. The kept entries of
+ * inv name distinct rows. An index outside its array is ignored (as a dropped
+ * pair) and sets MOE_DEV_BAD_INDEX.
+ * Rows are contiguous, of the context's H or I columns unless stated, and
+ * every tensor of rows, weights or codes is 16-byte aligned. Outputs may not
+ * overlap inputs. fp32 sums run in a fixed order, so results repeat bit for
+ * bit. These calls run on the context's device whatever device is current;
+ * `stream` belongs to that device. They take no workspace unless stated, and
+ * may be captured. */
+
+/* Row types of the training calls. */
+typedef enum {
+  MOE_T_BF16 = 0,
+  MOE_T_F32 = 1,
+  MOE_T_E4M3_B128 = 2 /* e4m3 codes with one fp32 scale per 128 columns (moe_quantize_e4m3, block_rows = 1) */
+} moe_dtype_t;
+
+/* Dispatch: x_sorted[inv[t*K+k], :] = x[t, :].
+ *   x [T, H] bf16 (MOE_T_BF16) or fp32 (MOE_T_F32), copied; or e4m3 codes
+ *   (MOE_T_E4M3_B128) with x_scales [T, H/128], written as bf16(code * scale):
+ *   the activation checkpoint of x back in expert order. x_scales is NULL for
+ *   the other types. x_sorted [T*K, H], bf16 or fp32. */
+moe_status_t moe_dispatch(moe_ctx_t* ctx, const void* x, const float* x_scales, int dtype, const int32_t* inv, int T,
+                          void* x_sorted, moe_stream_t stream);
+
+/* Gradient of the dispatch, and of the router's input where dlogit is given:
+ *   dx[t, :] = sum_k dx_sorted[inv[t*K+k], :] + sum_k dlogit[t, k] * w_router[topk_idx[t, k], :]
+ * k ascending in fp32 (the rows first), rounded once.
+ *   dx_sorted [T*K, H], dx [T, H], both bf16 or both fp32; dlogit [T, K] fp32
+ *   (moe_route_bwd), topk_idx [T, K], w_router [E, H] fp32: all three, or all
+ *   NULL. A topk_idx outside [0, E) adds nothing and sets MOE_DEV_BAD_EXPERT. */
+moe_status_t moe_dispatch_bwd(moe_ctx_t* ctx, const void* dx_sorted, int dtype, const int32_t* inv,
+                              const float* dlogit, const int32_t* topk_idx, const float* w_router, int T, void* dx,
+                              moe_stream_t stream);
+
+/* Combine with the weights applied here (moe_combine takes rows that carry
+ * them): out[t, :] = sum_k topk_w[t, k] * y_sorted[inv[t*K+k], :], one fp32
+ * fused multiply-add per pair, k ascending, rounded once.
+ *   y_sorted [T*K, H], out [T, H]: both bf16 or both fp32; topk_w [T, K] fp32. */
+moe_status_t moe_combine_weighted(moe_ctx_t* ctx, const void* y_sorted, int dtype, const float* topk_w,
+                                  const int32_t* inv, int T, void* out, moe_stream_t stream);
+
+/* Its gradient: dy_sorted[inv[t*K+k], :] = topk_w[t, k] * dout[t, :] (one
+ * rounding) and dtopk_w[t, k] = <dout[t, :], y_sorted[inv[t*K+k], :]> (fp32).
+ *   dout [T, H], y_sorted and dy_sorted [T*K, H]: all bf16 or all fp32. */
+moe_status_t moe_combine_weighted_bwd(moe_ctx_t* ctx, const void* dout, const void* y_sorted, int dtype,
+                                      const float* topk_w, const int32_t* inv, int T, void* dy_sorted,
+                                      float* dtopk_w, moe_stream_t stream);
+
+/* SwiGLU with 8-bit checkpoints. Per row of gu [rows, 2I] bf16 (gate columns
+ * 0..I-1, up columns I..2I-1): h = bf16(silu(g) * u) from the row itself, and
+ * q [rows, 2I] e4m3, s [rows, 2I/128] fp32 as moe_quantize_e4m3 (block_rows 1)
+ * writes them, for moe_swiglu_ckpt_bwd. Rows: with inv [rows] (rows = T*K) the
+ * kept pairs' rows; with inv NULL all of them. 0 <= rows <= 65536*32. */
+moe_status_t moe_swiglu_ckpt(moe_ctx_t* ctx, const void* gu, const int32_t* inv, int rows, void* h, uint8_t* q,
+                             float* s, moe_stream_t stream);
+
+/* Its gradient, from the checkpoint: with g, u = code * scale, h = silu(g) u
+ * and dh [rows, I] bf16,
+ *   dgu [rows, 2I] bf16 = w * (dh u silu'(g) | dh silu(g))
+ * and, when topk_w [rows] (fp32, in pair order) is given, w is the pair's
+ * weight and dtopk_w [rows] (fp32, pair order) = <dh, h>, hw [rows, I] bf16 =
+ * w h (NULL: not wanted). dh is then the gradient before the weight: dout
+ * through the down product, unweighted; hw is what dout multiplies in the down
+ * weights' gradient. Without topk_w, w = 1 and hw, dtopk_w are NULL; topk_w
+ * needs inv, or rows in pair order. */
+moe_status_t moe_swiglu_ckpt_bwd(moe_ctx_t* ctx, const uint8_t* q, const float* s, const void* dh,
+                                 const float* topk_w, const int32_t* inv, int rows, void* dgu, void* hw,
+                                 float* dtopk_w, moe_stream_t stream);
+
+/* Bytes of workspace moe_route_bwd needs for T tokens (0 for a bad T). */
+size_t moe_route_bwd_workspace_size(const moe_ctx_t* ctx, int T);
+
+/* Gradient of moe_route through the weights (the choice of experts has none):
+ *   dlogit[t, k] = topk_w[t, k] * (dtopk_w[t, k] - sum_j topk_w[t, j] dtopk_w[t, j])
+ *   dw_router[e, :] = sum over the kept pairs (t, k) of expert e of dlogit[t, k] * x[t, :]
+ *   dlogit_bias[e]  = sum over the same pairs of dlogit[t, k]       (NULL: not wanted)
+ *   x [T, H] bf16 with x_scales NULL, or e4m3 codes with x_scales [T, H/128]
+ *   (x = code * scale); topk_w, dtopk_w, dlogit [T, K] fp32; offsets, perm_src,
+ *   perm_k from moe_permute; dw_router [E, H] fp32, dlogit_bias [E] fp32, both
+ *   written whole (zeros for experts without pairs). ws: 256-byte aligned;
+ *   calls that may overlap need workspaces of their own. */
+moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales, const float* topk_w,
+                           const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T,
+                           float* dlogit, float* dw_router, float* dlogit_bias, void* ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/* One product per expert over its sorted rows p = offsets[e] .. offsets[e+1]-1
+ * (tensor cores, fp32 accumulation, one rounding), w [E, n_out, n_in] bf16:
+ *   transposed == 0: out[p, :] = w[e] a[p, :]     a [P, n_in],  out [P, n_out]
+ *   transposed != 0: out[p, :] = w[e]^T a[p, :]   a [P, n_out], out [P, n_in]
+ * (the forward product and the gradient of its rows). Rows at and behind
+ * offsets[E] are left as they were. n_in, n_out multiples of 128, at most
+ * 16384; 0 <= P <= 65536*32; offsets [E+1] rising from 0 or more to at most P.
+ * An expert whose range is not inside [0, P] computes nothing and sets
+ * MOE_DEV_BAD_INDEX. */
+moe_status_t moe_expert_product(moe_ctx_t* ctx, const void* a, const void* w, const int32_t* offsets, int P, int n_in,
+                                int n_out, int transposed, void* out, moe_stream_t stream);
+
+/* Gradient of the weights: dw[e] = sum over p of expert e of dy[p, :] a[p, :]^T,
+ * dw [E, n_out, n_in] bf16 or fp32 (dtype MOE_T_BF16 / MOE_T_F32), written
+ * whole (zeros for experts without rows) or, with accumulate != 0 (fp32 only),
+ * added to what is there. dy [P, n_out], a [P, n_in] bf16; rows of other
+ * experts and behind offsets[E] may hold anything. Limits as above. */
+moe_status_t moe_expert_wgrad(moe_ctx_t* ctx, const void* dy, const void* a, const int32_t* offsets, int P, int n_in,
+                              int n_out, int dtype, int accumulate, void* dw, moe_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------ */
 
 /* Test hook for failure detection: launches one thread on `stream` that
@@ -361,7 +475,11 @@ typedef enum {
   MOE_PROF_QUANT = 6,   /* FP8 quantiser of h */
   MOE_PROF_COMBINE = 7, /* weighted combine */
   MOE_PROF_FFN_FUSED = 8, /* decode: gate/up + SwiGLU and down * weight in one launch */
-  MOE_PROF_KINDS = 9
+  MOE_PROF_ROWS = 9,      /* training: dispatch, weighted combine and their gradients */
+  MOE_PROF_SWIGLU = 10,   /* training: SwiGLU with 8-bit checkpoints, and its gradient */
+  MOE_PROF_ROUTE_BWD = 11, /* training: router gradient */
+  MOE_PROF_PRODUCT = 12,  /* training: expert products and weight gradients */
+  MOE_PROF_KINDS = 13
 } moe_prof_kind_t;
 
 moe_status_t moe_profile_enable(moe_ctx_t* ctx, int enable);

@@ -9,6 +9,8 @@ ABI in ``include/moe.h``); this package is argument marshalling only:
 * :mod:`.build`   -- nvcc build of ``libmoe.so`` in-tree.
 * :mod:`.ep`      -- the expert-parallel schedule over several GPUs (which
   libmoe call comes when, and the NCCL all-to-alls between them).
+* :mod:`.train`   -- one training step of the layer (which libmoe call comes
+  when, and what is kept in between).
 
 Importing the package does not load the library; the first call of a binding
 function does, and raises if ``libmoe.so`` is missing (there is no fallback).
@@ -22,10 +24,15 @@ from .binding import (  # noqa: F401
     MOE_LOC_HOST_PINNED,
     MOE_SLOTS_LRU,
     MOE_SLOTS_PER_CALL,
+    MOE_T_BF16,
+    MOE_T_E4M3_B128,
+    MOE_T_F32,
     MoeError,
     MoeLayer,
     lib,
     moe_combine,
+    moe_combine_weighted,
+    moe_combine_weighted_bwd,
     moe_ctx_create,
     moe_ctx_destroy,
     MOE_ALLOC_ANY,
@@ -33,10 +40,14 @@ from .binding import (  # noqa: F401
     MOE_ALLOC_PINNED,
     moe_debug_fail_allocs,
     moe_debug_wait_flag,
+    moe_dispatch,
+    moe_dispatch_bwd,
     moe_ep_gather_rows,
     moe_ep_pack,
     moe_ep_recv_plan,
     moe_expert_ffn,
+    moe_expert_product,
+    moe_expert_wgrad,
     moe_forward,
     moe_get_device_status,
     moe_launch_count,
@@ -47,6 +58,8 @@ from .binding import (  # noqa: F401
     moe_quantize_e4m3,
     moe_quantize_mx,
     moe_route,
+    moe_route_bwd,
+    moe_route_bwd_workspace_size,
     moe_route_noalloc,
     moe_slots_create,
     moe_slots_destroy,
@@ -54,5 +67,7 @@ from .binding import (  # noqa: F401
     moe_slots_register,
     moe_slots_set_policy,
     moe_slots_stats,
+    moe_swiglu_ckpt,
+    moe_swiglu_ckpt_bwd,
     moe_workspace_size,
 )

@@ -8,6 +8,7 @@ CUDA stream unless one is given. Nothing is computed in Python; if
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -26,6 +27,10 @@ MOE_SLOTS_PER_CALL = 1
 MOE_DEV_BAD_EXPERT = 1
 MOE_DEV_NO_SLOT = 2
 MOE_DEV_TIMEOUT = 4
+MOE_DEV_BAD_INDEX = 8
+MOE_T_BF16 = 0
+MOE_T_F32 = 1
+MOE_T_E4M3_B128 = 2
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
                 4: "MOE_ERR_SLOT", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_OOM"}
@@ -36,9 +41,12 @@ EXPORTS = ["moe_ctx_create", "moe_ctx_destroy", "moe_workspace_size", "moe_route
            "moe_plan_hot_set", "moe_get_device_status", "moe_last_error", "moe_launch_count",
            "moe_profile_enable", "moe_profile_read", "moe_route_noalloc", "moe_slots_set_policy",
            "moe_debug_wait_flag", "moe_ep_pack", "moe_ep_recv_plan", "moe_ep_gather_rows", "moe_quantize_mx",
-           "moe_debug_fail_allocs"]
+           "moe_debug_fail_allocs", "moe_dispatch", "moe_dispatch_bwd", "moe_combine_weighted",
+           "moe_combine_weighted_bwd", "moe_swiglu_ckpt", "moe_swiglu_ckpt_bwd", "moe_route_bwd_workspace_size",
+           "moe_route_bwd", "moe_expert_product", "moe_expert_wgrad"]
 
-PROF_KINDS = ["router", "topk", "permute", "gather", "gate_up", "down", "quant", "combine", "ffn_fused"]
+PROF_KINDS = ["router", "topk", "permute", "gather", "gate_up", "down", "quant", "combine", "ffn_fused", "rows",
+              "swiglu", "route_bwd", "product"]
 
 
 class MoeError(RuntimeError):
@@ -99,6 +107,16 @@ def lib():
         "moe_ep_gather_rows": ([P, P, P, I, P, P], S),
         "moe_quantize_mx": ([P, I, I, I, P, P, P], S),
         "moe_debug_fail_allocs": ([I, I, I], S),
+        "moe_dispatch": ([P, P, P, I, P, I, P, P], S),
+        "moe_dispatch_bwd": ([P, P, I, P, P, P, P, I, P, P], S),
+        "moe_combine_weighted": ([P, P, I, P, P, I, P, P], S),
+        "moe_combine_weighted_bwd": ([P, P, P, I, P, P, I, P, P, P], S),
+        "moe_swiglu_ckpt": ([P, P, P, I, P, P, P, P], S),
+        "moe_swiglu_ckpt_bwd": ([P, P, P, P, P, P, I, P, P, P, P], S),
+        "moe_route_bwd_workspace_size": ([P, I], Z),
+        "moe_route_bwd": ([P, P, P, P, P, P, P, P, I, P, P, P, P, Z, P], S),
+        "moe_expert_product": ([P, P, P, P, I, I, I, I, P, P], S),
+        "moe_expert_wgrad": ([P, P, P, P, I, I, I, I, I, P, P], S),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -209,6 +227,55 @@ def moe_quantize_mx(src, rows, cols, elem, q, scales, stream=None):
     _check(lib().moe_quantize_mx(_p(src), rows, cols, elem, _p(q), _p(scales), _s(stream)), "moe_quantize_mx")
 
 
+def moe_dispatch(ctx, x, x_scales, dtype, inv, T, x_sorted, stream=None):
+    _check(lib().moe_dispatch(ctx, _p(x), _p(x_scales), dtype, _p(inv), T, _p(x_sorted), _s(stream)), "moe_dispatch")
+
+
+def moe_dispatch_bwd(ctx, dx_sorted, dtype, inv, dlogit, topk_idx, w_router, T, dx, stream=None):
+    _check(lib().moe_dispatch_bwd(ctx, _p(dx_sorted), dtype, _p(inv), _p(dlogit), _p(topk_idx), _p(w_router), T,
+                                  _p(dx), _s(stream)), "moe_dispatch_bwd")
+
+
+def moe_combine_weighted(ctx, y_sorted, dtype, topk_w, inv, T, out, stream=None):
+    _check(lib().moe_combine_weighted(ctx, _p(y_sorted), dtype, _p(topk_w), _p(inv), T, _p(out), _s(stream)),
+           "moe_combine_weighted")
+
+
+def moe_combine_weighted_bwd(ctx, dout, y_sorted, dtype, topk_w, inv, T, dy_sorted, dtopk_w, stream=None):
+    _check(lib().moe_combine_weighted_bwd(ctx, _p(dout), _p(y_sorted), dtype, _p(topk_w), _p(inv), T, _p(dy_sorted),
+                                          _p(dtopk_w), _s(stream)), "moe_combine_weighted_bwd")
+
+
+def moe_swiglu_ckpt(ctx, gu, inv, rows, h, q, s, stream=None):
+    _check(lib().moe_swiglu_ckpt(ctx, _p(gu), _p(inv), rows, _p(h), _p(q), _p(s), _s(stream)), "moe_swiglu_ckpt")
+
+
+def moe_swiglu_ckpt_bwd(ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dtopk_w, stream=None):
+    _check(lib().moe_swiglu_ckpt_bwd(ctx, _p(q), _p(s), _p(dh), _p(topk_w), _p(inv), rows, _p(dgu), _p(hw),
+                                     _p(dtopk_w), _s(stream)), "moe_swiglu_ckpt_bwd")
+
+
+def moe_route_bwd_workspace_size(ctx, T: int) -> int:
+    return int(lib().moe_route_bwd_workspace_size(ctx, T))
+
+
+def moe_route_bwd(ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dlogit, dw_router, dlogit_bias, ws,
+                  stream=None):
+    _check(lib().moe_route_bwd(ctx, _p(x), _p(x_scales), _p(topk_w), _p(dtopk_w), _p(offsets), _p(perm_src),
+                               _p(perm_k), T, _p(dlogit), _p(dw_router), _p(dlogit_bias), _p(ws), _nbytes(ws), _s(stream)),
+           "moe_route_bwd")
+
+
+def moe_expert_product(ctx, a, w, offsets, P, n_in, n_out, transposed, out, stream=None):
+    _check(lib().moe_expert_product(ctx, _p(a), _p(w), _p(offsets), P, n_in, n_out, int(transposed), _p(out),
+                                    _s(stream)), "moe_expert_product")
+
+
+def moe_expert_wgrad(ctx, dy, a, offsets, P, n_in, n_out, dtype, accumulate, dw, stream=None):
+    _check(lib().moe_expert_wgrad(ctx, _p(dy), _p(a), _p(offsets), P, n_in, n_out, dtype, int(accumulate), _p(dw),
+                                  _s(stream)), "moe_expert_wgrad")
+
+
 def moe_slots_create(ctx, n_spare_slots: int):
     h = ctypes.c_void_p()
     _check(lib().moe_slots_create(ctypes.byref(h), ctx, n_spare_slots), "moe_slots_create")
@@ -314,6 +381,15 @@ def _rows(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D [tokens, hidden] tensor")
     return x.shape[0]
+
+
+_ROW_TYPES = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_F32}
+
+
+def _row_type(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ROW_TYPES:
+        raise TypeError(f"{name}: expected a bf16 or fp32 tensor")
+    return _ROW_TYPES[t.dtype]
 
 
 class MoeLayer:
@@ -435,6 +511,193 @@ class MoeLayer:
         check_tensor(y_pair, "y_pair", torch.float32, (T * self.K, self.H), self.device)
         out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         moe_combine(self.ctx, y_pair, inv, T, out, stream)
+        return out
+
+    # ---- training: the pieces of one step (mixture_experts_layer_24_b200.train chains them) ----
+
+    def _on(self, stream):
+        """Where a training call allocates and launches: `stream` (a torch stream of this layer's device) or that
+        device's current stream. Results and temporaries belong to that stream."""
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            return torch.cuda.stream(stream)
+        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device)
+
+    def _out(self, t, name, dtype, shape):
+        """The caller's output tensor, checked, or a new one."""
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        check_tensor(t, name, dtype, shape, self.device)
+        return t
+
+    def dispatch(self, x, inv, x_scales=None, out=None, stream=None):
+        """Tokens in expert order, [T*K, H]: row inv[t, k] is x[t]. x is bf16 or fp32, or the e4m3 codes (uint8) of a
+        checkpoint with x_scales [T, H/128], which come back as bf16. Rows that no pair names are not written."""
+        T = _rows(x, "x")
+        if x_scales is None:
+            kind, dtype = _row_type(x, "x"), x.dtype
+        else:
+            kind, dtype = MOE_T_E4M3_B128, torch.bfloat16
+            check_tensor(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
+        check_tensor(x, "x", x.dtype if x_scales is None else torch.uint8, (T, self.H), self.device)
+        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
+        with self._on(stream):
+            out = self._out(out, "out", dtype, (T * self.K, self.H))
+            moe_dispatch(self.ctx, x, x_scales, kind, inv, T, out)
+        return out
+
+    def dispatch_bwd(self, dx_sorted, inv, dlogit=None, topk_idx=None, w_router=None, out=None, stream=None):
+        """dx [T, H]: each token's rows of dx_sorted [T*K, H] summed over k and, with dlogit [T, K] (from route_bwd),
+        topk_idx and w_router, what the router's logits pass back to its input."""
+        T = _rows(inv, "inv")
+        kind = _row_type(dx_sorted, "dx_sorted")
+        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
+        check_tensor(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * self.K, self.H), self.device)
+        if dlogit is not None or topk_idx is not None or w_router is not None:
+            check_tensor(dlogit, "dlogit", torch.float32, (T, self.K), self.device)
+            check_tensor(topk_idx, "topk_idx", torch.int32, (T, self.K), self.device)
+            check_tensor(w_router, "w_router", torch.float32, (self.E, self.H), self.device)
+        with self._on(stream):
+            out = self._out(out, "out", dx_sorted.dtype, (T, self.H))
+            moe_dispatch_bwd(self.ctx, dx_sorted, kind, inv, dlogit, topk_idx, w_router, T, out)
+        return out
+
+    def combine_weighted(self, y_sorted, topk_w, inv, out=None, stream=None):
+        """out [T, H] = sum over k of topk_w[t, k] * y_sorted[inv[t, k]] (bf16 or fp32 rows without their weight;
+        ``combine`` takes fp32 rows that carry it)."""
+        T = _rows(inv, "inv")
+        kind = _row_type(y_sorted, "y_sorted")
+        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
+        check_tensor(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
+        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        with self._on(stream):
+            out = self._out(out, "out", y_sorted.dtype, (T, self.H))
+            moe_combine_weighted(self.ctx, y_sorted, kind, topk_w, inv, T, out)
+        return out
+
+    def combine_weighted_bwd(self, dout, y_sorted, topk_w, inv, out=None, stream=None):
+        """(dy_sorted [T*K, H], dtopk_w [T, K]) of combine_weighted; `out` takes dy_sorted. Rows that no pair names
+        are not written."""
+        T = _rows(inv, "inv")
+        kind = _row_type(y_sorted, "y_sorted")
+        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
+        check_tensor(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
+        check_tensor(dout, "dout", y_sorted.dtype, (T, self.H), self.device)
+        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        with self._on(stream):
+            out = self._out(out, "out", y_sorted.dtype, (T * self.K, self.H))
+            dw = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+            moe_combine_weighted_bwd(self.ctx, dout, y_sorted, kind, topk_w, inv, T, out, dw)
+        return out, dw
+
+    def _pair_rows(self, t, name, inv):
+        rows = _rows(t, name)
+        if inv is not None:
+            check_tensor(inv, "inv", torch.int32, (rows // self.K, self.K), self.device)
+            if rows % self.K:
+                raise ValueError(f"{name}: {rows} rows are not a whole number of tokens of {self.K} pairs")
+        return rows
+
+    def swiglu_ckpt(self, gu, inv=None, out=None, stream=None):
+        """(h [rows, I] bf16, q [rows, 2I] uint8 e4m3 codes, s [rows, 2I/128] fp32): h = silu(g) * u of gu = [g | u]
+        bf16, and the 8-bit checkpoint that swiglu_ckpt_bwd reads. With inv, rows that no pair names are left alone.
+        `out` is a tuple of the three."""
+        rows, I = self._pair_rows(gu, "gu", inv), self.I
+        check_tensor(gu, "gu", torch.bfloat16, (rows, 2 * I), self.device)
+        h, q, s = out if out is not None else (None, None, None)
+        with self._on(stream):
+            h = self._out(h, "h", torch.bfloat16, (rows, I))
+            q = self._out(q, "q", torch.uint8, (rows, 2 * I))
+            s = self._out(s, "s", torch.float32, (rows, 2 * I // 128))
+            moe_swiglu_ckpt(self.ctx, gu, inv, rows, h, q, s)
+        return h, q, s
+
+    def swiglu_ckpt_bwd(self, q, s, dh, topk_w=None, inv=None, out=None, stream=None):
+        """(dgu [rows, 2I] bf16, hw, dtopk_w) from the checkpoint (q, s) and dh [rows, I] bf16. With topk_w [T, K],
+        dh is the gradient before the routing weight: dgu carries the weight, hw [rows, I] = w * h, dtopk_w [T, K] =
+        <dh, h>; without, the last two are None. `out` is a tuple (dgu, hw)."""
+        rows, I = self._pair_rows(dh, "dh", inv), self.I
+        check_tensor(dh, "dh", torch.bfloat16, (rows, I), self.device)
+        check_tensor(q, "q", torch.uint8, (rows, 2 * I), self.device)
+        check_tensor(s, "s", torch.float32, (rows, 2 * I // 128), self.device)
+        if topk_w is not None:
+            check_tensor(topk_w, "topk_w", torch.float32, (rows // self.K, self.K), self.device)
+            if rows % self.K:
+                raise ValueError(f"dh: {rows} rows are not a whole number of tokens of {self.K} pairs")
+        dgu, hw = out if out is not None else (None, None)
+        dw = None
+        with self._on(stream):
+            dgu = self._out(dgu, "dgu", torch.bfloat16, (rows, 2 * I))
+            if topk_w is not None:
+                hw = self._out(hw, "hw", torch.bfloat16, (rows, I))
+                dw = torch.empty((rows // self.K, self.K), dtype=torch.float32, device=self.device)
+            elif hw is not None:
+                raise ValueError("hw: only with topk_w")
+            moe_swiglu_ckpt_bwd(self.ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dw)
+        return dgu, hw, dw
+
+    def route_bwd(self, x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales=None, stream=None):
+        """(dlogit [T, K], dw_router [E, H], dlogit_bias [E]), all fp32: the gradient of ``route`` through its
+        weights; offsets, perm_src and perm_k are ``permute``'s. x is bf16, or the e4m3 codes (uint8) of its checkpoint
+        with x_scales [T, H/128]."""
+        T = _rows(x, "x")
+        P = T * self.K
+        check_tensor(x, "x", torch.bfloat16 if x_scales is None else torch.uint8, (T, self.H), self.device)
+        if x_scales is not None:
+            check_tensor(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
+        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        check_tensor(dtopk_w, "dtopk_w", torch.float32, (T, self.K), self.device)
+        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        check_tensor(perm_src, "perm_src", torch.int32, (P,), self.device)
+        check_tensor(perm_k, "perm_k", torch.int32, (P,), self.device)
+        with self._on(stream):
+            ws = torch.empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8, device=self.device)
+            dl = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+            dwr = torch.empty((self.E, self.H), dtype=torch.float32, device=self.device)
+            db = torch.empty((self.E,), dtype=torch.float32, device=self.device)
+            moe_route_bwd(self.ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dl, dwr, db, ws)
+        return dl, dwr, db
+
+    def _weights_shape(self, w, name):
+        if not isinstance(w, torch.Tensor) or w.dim() != 3:
+            raise ValueError(f"{name}: expected a 3-D [experts, n_out, n_in] tensor")
+        return int(w.shape[1]), int(w.shape[2])
+
+    def expert_product(self, a, w, offsets, transposed=False, out=None, stream=None):
+        """Each expert's rows of a (sorted, offsets from ``permute``) times its weights w [E, n_out, n_in] bf16:
+        a [P, n_in] -> [P, n_out], or with transposed a [P, n_out] -> [P, n_in] (the gradient of the rows). Rows
+        behind the last expert's are not written."""
+        P = _rows(a, "a")
+        n_out, n_in = self._weights_shape(w, "w")
+        k, m = (n_out, n_in) if transposed else (n_in, n_out)
+        check_tensor(w, "w", torch.bfloat16, (self.E, n_out, n_in), self.device)
+        check_tensor(a, "a", torch.bfloat16, (P, k), self.device)
+        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        with self._on(stream):
+            out = self._out(out, "out", torch.bfloat16, (P, m))
+            moe_expert_product(self.ctx, a, w, offsets, P, n_in, n_out, transposed, out)
+        return out
+
+    def expert_wgrad(self, dy, a, offsets, dtype=torch.bfloat16, out=None, accumulate=False, stream=None):
+        """dw [E, n_out, n_in] = each expert's dy^T a over its rows (dy [P, n_out], a [P, n_in] bf16), bf16 or fp32;
+        with accumulate, added to the fp32 tensor `out`."""
+        P, n_out = _rows(dy, "dy"), int(dy.shape[1])
+        n_in = int(a.shape[1]) if isinstance(a, torch.Tensor) and a.dim() == 2 else -1
+        check_tensor(dy, "dy", torch.bfloat16, (P, n_out), self.device)
+        check_tensor(a, "a", torch.bfloat16, (P, n_in), self.device)
+        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        if out is not None:
+            dtype = out.dtype
+        elif accumulate:
+            raise ValueError("accumulate: needs the tensor to add to (out)")
+        if dtype not in _ROW_TYPES:
+            raise TypeError("dtype: expected bf16 or fp32")
+        with self._on(stream):
+            out = self._out(out, "out", dtype, (self.E, n_out, n_in))
+            moe_expert_wgrad(self.ctx, dy, a, offsets, P, n_in, n_out, _ROW_TYPES[dtype], accumulate, out)
         return out
 
     def capture(self, x, w_router, logit_bias=None):

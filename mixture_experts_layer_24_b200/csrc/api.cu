@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "ctx.h"
 #include "internal.h"
 
 using namespace moe;
@@ -40,91 +41,11 @@ moe_status_t fail(moe_status_t st, const std::string& msg) {
   return st;
 }
 
-#define MOE_CUDA(call)                                                                              \
-  do {                                                                                              \
-    cudaError_t err_ = (call);                                                                      \
-    if (err_ != cudaSuccess)                                                                        \
-      return fail(MOE_ERR_CUDA, std::string(#call) + ": " + cudaGetErrorString(err_));             \
-  } while (0)
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
 void moe::record_error(const char* msg) { g_last_error = msg ? msg : ""; }
-
-struct moe_ctx {
-  moe_config_t cfg;
-  int device = 0;
-  int* d_status = nullptr;
-  int num_sms = 148;
-  bool chain = true;  // programmatic dependent launch between this library's kernels
-  unsigned int* d_counters = nullptr;  // arrival counters of the decode router (self-resetting)
-  int host_status = 0;
-  EncodeTiledFn encode = nullptr;
-  std::atomic<int64_t> launches{0};
-  // kernel timing (moe_profile_*)
-  bool prof_on = false;
-  struct Rec {
-    int kind;
-    cudaEvent_t a, b;
-  };
-  std::vector<Rec> prof_pending;
-  std::vector<cudaEvent_t> ev_pool;
-  double prof_ms[MOE_PROF_KINDS] = {};
-  int64_t prof_n[MOE_PROF_KINDS] = {};
-  std::mutex prof_mu;
-
-  cudaEvent_t take_event() {
-    if (!ev_pool.empty()) {
-      cudaEvent_t e = ev_pool.back();
-      ev_pool.pop_back();
-      return e;
-    }
-    cudaEvent_t e = nullptr;
-    cudaEventCreate(&e);
-    return e;
-  }
-};
-
-namespace {
-// Step names of the MOE_PROF_* kinds, for the NVTX ranges below.
-static const char* const kStepNames[MOE_PROF_KINDS] = {"moe.router",  "moe.topk", "moe.permute",
-                                                       "moe.gather",  "moe.gate_up", "moe.down",
-                                                       "moe.quant",   "moe.combine", "moe.ffn_fused"};
-
-// Counts one kernel launch, names it with an NVTX range on the host timeline
-// (free unless a profiler is attached), and, when timing is on, brackets it
-// with events on the launching stream.
-struct Prof {
-  moe_ctx* c;
-  int kind;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr;
-  Prof(moe_ctx* c_, int kind_, cudaStream_t s_) : c(c_), kind(kind_), s(s_) {
-    nvtxRangePushA(kStepNames[kind]);
-    if (c->prof_on) {
-      std::lock_guard<std::mutex> g(c->prof_mu);
-      a = c->take_event();
-      cudaEventRecord(a, s);
-    }
-  }
-  ~Prof() {
-    nvtxRangePop();
-    c->launches.fetch_add(1, std::memory_order_relaxed);
-    if (a) {
-      std::lock_guard<std::mutex> g(c->prof_mu);
-      cudaEvent_t b = c->take_event();
-      cudaEventRecord(b, s);
-      c->prof_pending.push_back({kind, a, b});
-    }
-  }
-};
-}  // namespace
 
 struct moe_slots {
   moe_ctx* ctx = nullptr;

@@ -1,0 +1,520 @@
+// expert_product.cu -- the per-expert products of a training step on the
+// 5th-generation tensor cores. The rows of expert e are the sorted pairs
+// p = offsets[e] .. offsets[e+1]-1; every output element is one fp32
+// accumulation over its whole K axis, in increasing order, rounded once:
+//
+//   forward   out[p, o] = sum_i a[p, i] * w[e, o, i]     a [P, n_in],  w [E, n_out, n_in]
+//   rows' gradient
+//             out[p, i] = sum_o a[p, o] * w[e, o, i]     a [P, n_out]
+//   weights' gradient
+//             dw[e, o, i] = sum_{p of e} dy[p, o] * a[p, i]
+//
+// Two CTAs of a cluster (one TPC) compute one 256 x 256 tile with
+// cta_group::2: each stages 128 rows of the M operand and half of the N
+// operand (32 KB per 64-deep K step), so a pair moves half the bytes from L2
+// that two separate 128 x 256 tiles would. M is the feature axis, so its tiles
+// are always full; N is the expert's rows in the first two forms (the MMA
+// width follows the rows left, in steps of 32), the input features in the
+// third.
+//
+// Operands come by TMA in 128-byte swizzled boxes of 64 elements. Where the
+// K axis is the contiguous one in memory (forward: both; rows' gradient: a)
+// the box is K-major; where it is the row axis (the weights in the rows'
+// gradient, both operands of the weights' gradient) the box is MN-major and
+// the MMA reads it transposed, so nothing is ever transposed in memory.
+//
+// In the weights' gradient K is the expert's own rows: the last K step of an
+// expert may hold rows of the next one (or of no expert at all, with any
+// bits in them). Those rows are zeroed in shared memory, in both operands,
+// before the MMA of that step sees them, by a warp of its own; K-16 steps
+// with no row of the expert are not issued.
+//
+// Warp roles: 0..3 epilogue (TMEM -> registers -> global), 4 TMA producer,
+// 5 TMEM allocation and, in the leader CTA, the MMA issuer, 6 the tail's
+// zero writer. Persistent; two TMEM accumulators of 256 columns, so a tile's
+// epilogue overlaps the next tile's MMAs. Every wait is bounded.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTileM = 256;  // features per CTA pair
+constexpr int kTileN = 256;
+constexpr int kStages = 6;
+constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
+constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
+constexpr int kThreads = 224;
+constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
+
+enum Form { kForward = 0, kRowGrad = 1, kWeightGrad = 2 };
+
+// ------------------------------------------------------- cluster helpers --
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The shared::cluster address of `addr` (this CTA's offset) in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void remote_arrive(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void remote_expect_tx(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
+               "r"(bytes)
+               : "memory");
+}
+
+// Bounded wait whose acquire covers the other CTA of the cluster.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// TMA load into this CTA's shared memory; the bytes complete on a barrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, uint32_t cluster_bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(cluster_bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One arrival on `bar` in both CTAs once this thread's MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// MN-major operand in 128-byte swizzled boxes of 64 K rows x 64 elements:
+// groups of 8 K rows 1024 bytes apart (stride byte offset), the next 64
+// elements one box further (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+struct Tile {
+  int e, m0, row0, rows, n0, n;  // n0, n: first column and width of the N axis (weights' gradient: input features)
+};
+
+// Rows of expert e, clamped so that a bad offsets entry never leads outside [0, P).
+__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int P, int& row0, int& rows,
+                                            int* status) {
+  const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+  if (a < 0 || b < a || b > P) {
+    flag_status(status, MOE_DEV_BAD_INDEX);
+    row0 = rows = 0;
+    return;
+  }
+  row0 = a;
+  rows = b - a;
+}
+
+}  // namespace
+
+template <int FORM>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_product_kernel(const __grid_constant__ ProductMaps maps, const ProductArgs a) {
+  constexpr bool kWG = FORM == kWeightGrad;
+  constexpr bool kMmn = FORM != kForward;  // the M operand is MN-major
+  constexpr bool kNmn = kWG;               // so is the N operand
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const int m_tiles = (a.m_total + kTileM - 1) / kTileM;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + kStages * kStageBytes;
+  auto full = [&](int s) { return bars + 8u * s; };  // in the leader CTA; one arrival per CTA and the bytes of both
+  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto landed = [&](int s) { return bars + 8u * (2 * kStages + s); };  // tail steps, before the zeros
+  auto tfull = [&](int b) { return bars + 8u * (3 * kStages + b); };
+  auto tempty = [&](int b) { return bars + 8u * (3 * kStages + 2 + b); };  // in the leader CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kStages * kStageBytes + 8 * (3 * kStages + 4));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* prefix = reinterpret_cast<int*>(tmem_slot + 4);  // [E + 1] N tiles before each expert (not in kWG)
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 2);
+      mbar_init(empty(s), 1);
+      mbar_init(landed(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), 8);  // four epilogue warps of each CTA
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tmem_alloc2(smem_u32(tmem_slot), 512);
+  if (!kWG && warp == 6) {
+    int run = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      int nt = 0;
+      if (e0 + lane < a.E) {
+        int r0, rows;
+        expert_rows(a.offsets, e0 + lane, a.P, r0, rows, a.status);
+        nt = (rows + kTileN - 1) / kTileN;
+      }
+      int incl = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (e0 + lane < a.E) prefix[e0 + lane] = run + incl - nt;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[a.E] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  const int n_tiles_w = (a.n_total + kTileN - 1) / kTileN;  // kWG: N tiles of one expert
+  const int total = kWG ? a.E * m_tiles * n_tiles_w : prefix[a.E] * m_tiles;
+  auto decode = [&](int tile) {
+    Tile t;
+    if (kWG) {
+      const int per = m_tiles * n_tiles_w;
+      t.e = tile / per;
+      const int r = tile - t.e * per;
+      t.m0 = (r / n_tiles_w) * kTileM;
+      t.n0 = (r % n_tiles_w) * kTileN;
+      t.n = min(kTileN, a.n_total - t.n0);
+      expert_rows(a.offsets, t.e, a.P, t.row0, t.rows, nullptr);
+    } else {
+      int lo = 0, hi = a.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] * m_tiles <= tile) lo = mid;
+        else hi = mid;
+      }
+      const int nti = prefix[lo + 1] - prefix[lo];
+      const int r = tile - prefix[lo] * m_tiles;
+      int row0, rows;
+      expert_rows(a.offsets, lo, a.P, row0, rows, nullptr);
+      t.e = lo;
+      t.m0 = (r / nti) * kTileM;
+      const int nt = r % nti;
+      t.row0 = row0 + nt * kTileN;
+      t.rows = min(kTileN, rows - nt * kTileN);
+      t.n0 = 0;
+      t.n = (t.rows + 31) & ~31;
+    }
+    return t;
+  };
+  auto k_steps = [&](const Tile& t) { return kWG ? (t.rows + 63) / 64 : a.k_total / 64; };
+
+  if (warp == 4) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      int issued = 0;
+      for (int tile = cluster; tile < total && !*abort_flag; tile += n_clusters) {
+        const Tile t = decode(tile);
+        const int KB = k_steps(t);
+        const int half = t.n / 2;  // this CTA's part of the N operand
+        const int mrow = t.m0 + (int)rank * 128;
+        // K-major N operand: one box of 16, 32, 64 or 128 rows
+        const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const uint32_t bytes = kOpBytes + (kNmn ? (uint32_t)(half / 64) * kBoxBytes : (16u << bi) * 128u);
+        for (int kb = 0; kb < KB; ++kb, ++issued) {
+          const int s = issued % kStages;
+          if (issued >= kStages && !mbar_wait(empty(s), ((issued / kStages) - 1) & 1)) {
+            *abort_flag = 1;
+            flag_status(a.status, MOE_DEV_TIMEOUT);
+            break;
+          }
+          const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
+          const bool tail = kWG && kb == KB - 1 && (t.rows & 63);
+          uint32_t bar;
+          if (tail) {
+            bar = map_rank(landed(s), rank);
+            mbar_arrive_expect_tx(landed(s), bytes);
+          } else {
+            bar = map_rank(full(s), 0);
+            remote_expect_tx(bar, bytes);
+          }
+          if (FORM == kForward) {
+            tma_load_pair(sa, &maps.m, bar, kb * 64, t.e * a.m_total + mrow);
+          } else {
+            const int row = kWG ? t.row0 + kb * 64 : t.e * a.k_total + kb * 64;
+            tma_load_pair(sa, &maps.m, bar, mrow, row);
+            tma_load_pair(sa + kBoxBytes, &maps.m, bar, mrow + 64, row);
+          }
+          if (kNmn) {
+            for (int j = 0; j < half / 64; ++j)
+              tma_load_pair(sb + j * kBoxBytes, &maps.n[0], bar, t.n0 + (int)rank * half + 64 * j,
+                            t.row0 + kb * 64);
+          } else {
+            tma_load_pair(sb, &maps.n[bi], bar, kb * 64, t.row0 + (int)rank * half);
+          }
+        }
+      }
+      // copies of the pair have landed before the leader goes on to the last cluster barrier
+      if (rank == 0)
+        for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
+          wait_cluster(full(g % kStages), (g / kStages) & 1);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0 && lane == 0) {
+      int consumed = 0, j = 0;
+      for (int tile = cluster; tile < total; tile += n_clusters) {
+        const Tile t = decode(tile);
+        const int KB = k_steps(t);
+        if (KB == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const int buf = j & 1;
+        bool ok = j < 2 || wait_cluster(tempty(buf), ((j >> 1) - 1) & 1);
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kTileN;
+        const uint32_t idesc =
+            instr_desc(256, t.n, 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
+        for (int kb = 0; ok && kb < KB; ++kb, ++consumed) {
+          const int s = consumed % kStages;
+          if (!wait_cluster(full(s), (consumed / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
+          const int left = t.rows - kb * 64;
+          const int ks = kWG ? (left >= 64 ? 4 : (left + 15) / 16) : 4;
+#pragma unroll 4
+          for (int k = 0; k < ks; ++k) {
+            const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048) : sw128_kmajor_desc(sa + k * 32);
+            const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048) : sw128_kmajor_desc(sb + k * 32);
+            mma_pair(d, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          commit_pair(empty(s));
+        }
+        commit_pair(tfull(buf));
+        if (!ok) {
+          *abort_flag = 1;
+          flag_status(a.status, MOE_DEV_TIMEOUT);
+          break;
+        }
+        ++j;
+      }
+    }
+  } else if (warp == 6) {
+    // --------------------------------------------- zeros of the tail K steps
+    if (kWG) {
+      int before = 0;
+      uint32_t phases = 0;  // bit s: parity of the next use of landed(s)
+      for (int tile = cluster; tile < total; tile += n_clusters) {
+        const Tile t = decode(tile);
+        const int KB = k_steps(t);
+        before += KB;
+        const int rem = t.rows & 63;
+        if (rem == 0) continue;
+        const int s = (before - 1) % kStages;
+        // every lane waits itself: each writes over bytes that the copy brought
+        const int ok = __all_sync(0xffffffffu, mbar_wait(landed(s), (phases >> s) & 1));
+        phases ^= 1u << s;
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            flag_status(a.status, MOE_DEV_TIMEOUT);
+          }
+          break;
+        }
+        const int upto = (rem + 15) & ~15;
+        const int boxes = 2 + t.n / 128;  // M operand, then this CTA's part of the N operand
+        const int vecs = (upto - rem) * 8;
+        for (int b = 0; b < boxes; ++b) {
+          uint8_t* box = gbase + s * kStageBytes + b * kBoxBytes + rem * 128;
+          for (int v = lane; v < vecs; v += 32) *reinterpret_cast<uint4*>(box + v * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) remote_arrive(map_rank(full(s), 0));
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    int j = 0;
+    for (int tile = cluster; tile < total; tile += n_clusters) {
+      const Tile t = decode(tile);
+      const int KB = k_steps(t);
+      const int f = t.m0 + (int)rank * 128 + warp * 32 + lane;  // this lane's feature (M axis)
+      const bool in_m = t.m0 + (int)rank * 128 < a.m_total;     // CTA-uniform
+      const int buf = j & 1;
+      if (KB > 0) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(tfull(buf), (j >> 1) & 1) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            flag_status(a.status, MOE_DEV_TIMEOUT);
+          }
+          break;
+        }
+        tc_fence_after();
+      }
+      if (in_m) {
+        const uint32_t tl = tmem + buf * kTileN + (static_cast<uint32_t>(warp * 32) << 16);
+        const int cols = kWG ? t.n : t.rows;
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32];
+          if (KB > 0) {
+            tmem_ld32(tl + c, v);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = 0u;
+          }
+          if (kWG) {
+            const size_t at = ((size_t)t.e * a.m_total + f) * a.n_total + t.n0 + c;
+            if (a.out_f32) {
+              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                float4 w = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                       __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+                if (a.accumulate) {
+                  const float4 old = o[q];
+                  w.x += old.x, w.y += old.y, w.z += old.z, w.w += old.w;
+                }
+                o[q] = w;
+              }
+            } else {
+              uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * i]),
+                                                                  __uint_as_float(v[8 * q + 2 * i + 1]));
+                  w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)(t.row0 + c) * a.m_total + f;
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (c + q < cols) out[(size_t)q * a.m_total] = __float2bfloat16_rn(__uint_as_float(v[q]));
+          }
+        }
+      }
+      if (KB > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
+        ++j;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs are done with each other's barriers and with TMEM
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+}
+
+namespace {
+template <int FORM>
+cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long max_tiles, int num_sms,
+                        cudaStream_t s) {
+  const size_t smem = 1024 + (size_t)kStages * kStageBytes + 8 * (3 * kStages + 4) + 16 + 4 * (a.E + 1);
+  const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const long long clusters = std::max(1LL, std::min<long long>(num_sms / 2, max_tiles));
+  expert_product_kernel<FORM><<<dim3((unsigned)(2 * clusters)), dim3(kThreads), smem, s>>>(maps, a);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_expert_product(int form, const ProductMaps& maps, const ProductArgs& a, int num_sms,
+                                  cudaStream_t s) {
+  const long long m_tiles = (a.m_total + kTileM - 1) / kTileM;
+  const long long rows_tiles = (a.P + kTileN - 1) / kTileN + std::min(a.E, a.P);
+  if (form == kForward) return launch_form<kForward>(maps, a, rows_tiles * m_tiles, num_sms, s);
+  if (form == kRowGrad) return launch_form<kRowGrad>(maps, a, rows_tiles * m_tiles, num_sms, s);
+  return launch_form<kWeightGrad>(maps, a, (long long)a.E * m_tiles * ((a.n_total + kTileN - 1) / kTileN), num_sms,
+                                  s);
+}
+
+}  // namespace moe

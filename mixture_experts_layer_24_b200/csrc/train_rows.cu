@@ -1,0 +1,215 @@
+// train_rows.cu -- tokens to expert order and back in a training step, and the
+// gradients of both. Pair i = t*K + k; inv[i] is its row in expert order, -1
+// for a dropped pair (it takes no part). Sums run k ascending in fp32 and are
+// rounded once.
+//
+//   dispatch              xs[inv[t,k], :] = x[t, :]
+//                         (x bf16 or fp32: copied; x an e4m3 checkpoint:
+//                         bf16(code * scale), scales per 1 x 128 block)
+//   its gradient          dx[t, :] = sum_k dxs[inv[t,k], :] + dl[t,k] * Wr[idx[t,k], :]
+//                         (the second term when the router's logits pass a gradient back)
+//   weighted combine      out[t, :] = sum_k w[t,k] * y[inv[t,k], :]
+//   its gradient          dy[inv[t,k], :] = w[t,k] * dout[t, :],  dw[t,k] = <dout[t, :], y[inv[t,k], :]>
+//
+// All are bound by HBM. Each kernel touches a token's row once and the token's
+// K expert rows once: a thread owns one 16-byte piece of a token's row and
+// walks the K rows (dispatch, its gradient, the combine), or a warp owns one
+// pair (the combine's gradient, where each pair needs a dot product over the
+// whole row and the token's row is shared by neighbouring warps).
+#include "internal.h"
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSlots = 8;  // pairs whose rows are in flight per thread
+
+// One thread per 16-byte piece of the output row.
+template <class R, bool kCkpt>
+__global__ void __launch_bounds__(256) dispatch_kernel(const void* __restrict__ x, const float* __restrict__ scales,
+                                                        const int32_t* __restrict__ inv, int T, int K, unsigned V,
+                                                        uint4* __restrict__ xs, int* status) {
+  const unsigned i = blockIdx.x * 256u + threadIdx.x;
+  const unsigned t = i / V, v = i - t * V;
+  if (t >= (unsigned)T) return;
+  uint4 piece;
+  if (kCkpt) {
+    const uint2 q = __ldg(static_cast<const uint2*>(x) + (size_t)t * V + v);
+    float f[8];
+    e4m3x8(q, __ldg(scales + (size_t)t * (V / 16) + v / 16), f);
+    piece = RowBf16::pack(f);
+  } else {
+    piece = __ldg(static_cast<const uint4*>(x) + (size_t)t * V + v);
+  }
+  const int P = T * K;
+  for (int k = 0; k < K; ++k) {
+    const int p = pair_row(inv, (long long)t * K + k, P, status);
+    if (p >= 0) xs[(size_t)p * V + v] = piece;
+  }
+}
+
+// kWeighted: out = sum_k w y (the combine). Otherwise the dispatch's gradient,
+// with the router's term when dl is given.
+template <class R, bool kWeighted>
+__global__ void __launch_bounds__(256) gather_sum_kernel(const uint4* __restrict__ rows,
+                                                          const float* __restrict__ w,
+                                                          const int32_t* __restrict__ inv,
+                                                          const float* __restrict__ dl,
+                                                          const int32_t* __restrict__ idx,
+                                                          const float* __restrict__ wr, int T, int K, int E, unsigned V,
+                                                          uint4* __restrict__ out, int* status) {
+  const unsigned i = blockIdx.x * 256u + threadIdx.x;
+  const unsigned t = i / V, v = i - t * V;
+  if (t >= (unsigned)T) return;
+  const int P = T * K;
+  float acc[R::kN];
+#pragma unroll
+  for (int j = 0; j < R::kN; ++j) acc[j] = 0.0f;
+  for (int k0 = 0; k0 < K; k0 += kSlots) {
+    int p[kSlots];
+    uint4 a[kSlots];
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) p[u] = k0 + u < K ? pair_row(inv, (long long)t * K + k0 + u, P, status) : -1;
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u)
+      if (p[u] >= 0) a[u] = __ldg(rows + (size_t)p[u] * V + v);
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) {
+      if (p[u] < 0) continue;
+      float f[R::kN];
+      R::unpack(a[u], f);
+      const float wk = kWeighted ? __ldg(w + (size_t)t * K + k0 + u) : 1.0f;
+#pragma unroll
+      for (int j = 0; j < R::kN; ++j) acc[j] = kWeighted ? fmaf(wk, f[j], acc[j]) : acc[j] + f[j];
+    }
+  }
+  if (!kWeighted && dl) {
+    const int H = (int)V * R::kN;
+    for (int k = 0; k < K; ++k) {
+      const int e = __ldg(idx + (size_t)t * K + k);
+      if (e < 0 || e >= E) {
+        flag_status(status, MOE_DEV_BAD_EXPERT);
+        continue;
+      }
+      const float d = __ldg(dl + (size_t)t * K + k);
+      const float4* r = reinterpret_cast<const float4*>(wr + (size_t)e * H + v * R::kN);
+#pragma unroll
+      for (int j = 0; j < R::kN / 4; ++j) {
+        const float4 q = __ldg(r + j);
+        acc[4 * j] = fmaf(d, q.x, acc[4 * j]);
+        acc[4 * j + 1] = fmaf(d, q.y, acc[4 * j + 1]);
+        acc[4 * j + 2] = fmaf(d, q.z, acc[4 * j + 2]);
+        acc[4 * j + 3] = fmaf(d, q.w, acc[4 * j + 3]);
+      }
+    }
+  }
+  out[(size_t)t * V + v] = R::pack(acc);
+}
+
+// One warp per pair.
+template <class R>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ y,
+                                                           const float* __restrict__ w,
+                                                           const int32_t* __restrict__ inv, int T, int K, int V,
+                                                           uint4* __restrict__ dy, float* __restrict__ dw,
+                                                           int* status) {
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= (long long)T * K) return;
+  const int p = pair_row(inv, i, T * K, status);
+  if (p < 0) {
+    if (lane == 0) dw[i] = 0.0f;
+    return;
+  }
+  const int t = (int)(i / K);
+  const float wk = __ldg(w + i);
+  const uint4* d = dout + (size_t)t * V;
+  const uint4* r = y + (size_t)p * V;
+  uint4* o = dy + (size_t)p * V;
+  float dot = 0.0f;
+  for (int v0 = lane; v0 < V; v0 += 32 * 4) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v0 + 32 * u < V) {
+        a[u] = __ldg(d + v0 + 32 * u);
+        b[u] = __ldg(r + v0 + 32 * u);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v0 + 32 * u < V) {
+        float fa[R::kN], fb[R::kN];
+        R::unpack(a[u], fa);
+        R::unpack(b[u], fb);
+#pragma unroll
+        for (int j = 0; j < R::kN; ++j) {
+          dot = fmaf(fa[j], fb[j], dot);
+          fa[j] *= wk;
+        }
+        o[v0 + 32 * u] = R::pack(fa);
+      }
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+  if (lane == 0) dw[i] = dot;
+}
+
+unsigned blocks_for(long long n) { return (unsigned)((n + 255) / 256); }
+
+}  // namespace
+
+cudaError_t launch_dispatch(const void* x, const float* scales, int dtype, const int32_t* inv, int T, int K, int H,
+                            void* xs, int* status, cudaStream_t s) {
+  uint4* o = static_cast<uint4*>(xs);
+  const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
+  const unsigned blocks = blocks_for((long long)T * V);
+  if (dtype == MOE_T_E4M3_B128)
+    dispatch_kernel<RowBf16, true><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
+  else
+    dispatch_kernel<RowBf16, false><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch_bwd(const void* rows, int dtype, const int32_t* inv, const float* dl, const int32_t* idx,
+                                const float* wr, int T, int K, int E, int H, void* dx, int* status, cudaStream_t s) {
+  const uint4* r = static_cast<const uint4*>(rows);
+  uint4* o = static_cast<uint4*>(dx);
+  const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
+  const unsigned blocks = blocks_for((long long)T * V);
+  if (dtype == MOE_T_F32)
+    gather_sum_kernel<RowF32, false><<<blocks, 256, 0, s>>>(r, nullptr, inv, dl, idx, wr, T, K, E, V, o, status);
+  else
+    gather_sum_kernel<RowBf16, false><<<blocks, 256, 0, s>>>(r, nullptr, inv, dl, idx, wr, T, K, E, V, o, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_weighted(const void* y, int dtype, const float* w, const int32_t* inv, int T, int K, int H,
+                                    void* out, int* status, cudaStream_t s) {
+  const uint4* r = static_cast<const uint4*>(y);
+  uint4* o = static_cast<uint4*>(out);
+  const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
+  const unsigned blocks = blocks_for((long long)T * V);
+  if (dtype == MOE_T_F32)
+    gather_sum_kernel<RowF32, true><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o, status);
+  else
+    gather_sum_kernel<RowBf16, true><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o,
+                                                            status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_weighted_bwd(const void* dout, const void* y, int dtype, const float* w,
+                                        const int32_t* inv, int T, int K, int H, void* dy, float* dw, int* status,
+                                        cudaStream_t s) {
+  const int V = dtype == MOE_T_F32 ? H / 4 : H / 8;
+  const unsigned blocks = (unsigned)(((long long)T * K + 7) / 8);
+  const uint4 *d = static_cast<const uint4*>(dout), *r = static_cast<const uint4*>(y);
+  uint4* o = static_cast<uint4*>(dy);
+  if (dtype == MOE_T_F32)
+    combine_bwd_kernel<RowF32><<<blocks, 256, 0, s>>>(d, r, w, inv, T, K, V, o, dw, status);
+  else
+    combine_bwd_kernel<RowBf16><<<blocks, 256, 0, s>>>(d, r, w, inv, T, K, V, o, dw, status);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,214 @@
+"""Training operators without a GPU: what the entry points refuse, and the
+gradient formulas against differences of the forward."""
+
+import pytest
+import torch
+
+import train_ref as R
+
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from mixture_experts_layer_24_b200 import build as B
+    B.build()
+    import mixture_experts_layer_24_b200 as M
+    return M.lib()
+
+
+def test_null_contexts_are_refused(lib):
+    N = None
+    assert lib.moe_dispatch(N, N, N, 0, N, 1, N, N) == 1
+    assert lib.moe_dispatch_bwd(N, N, 0, N, N, N, N, 1, N, N) == 1
+    assert lib.moe_combine_weighted(N, N, 0, N, N, 1, N, N) == 1
+    assert lib.moe_combine_weighted_bwd(N, N, N, 0, N, N, 1, N, N, N) == 1
+    assert lib.moe_swiglu_ckpt(N, N, N, 1, N, N, N, N) == 1
+    assert lib.moe_swiglu_ckpt_bwd(N, N, N, N, N, N, 1, N, N, N, N) == 1
+    assert lib.moe_route_bwd_workspace_size(N, 4) == 0
+    assert lib.moe_route_bwd(N, N, N, N, N, N, N, N, 1, N, N, N, N, 0, N) == 1
+    assert lib.moe_expert_product(N, N, N, N, 1, 128, 128, 0, N, N) == 1
+    assert lib.moe_expert_wgrad(N, N, N, N, 1, 128, 128, 0, 0, N, N) == 1
+    assert b"NULL context" in lib.moe_last_error()
+
+
+CALLS = ("moe_dispatch", "moe_dispatch_bwd", "moe_combine_weighted", "moe_combine_weighted_bwd", "moe_swiglu_ckpt",
+         "moe_swiglu_ckpt_bwd", "moe_route_bwd", "moe_expert_product", "moe_expert_wgrad", "moe_route", "moe_permute",
+         "moe_quantize_e4m3")
+
+
+@pytest.fixture
+def host_layer(monkeypatch):
+    """A layer on the host whose C calls only note that they were reached: argument checks and allocation run."""
+    from mixture_experts_layer_24_b200 import binding as B
+    from mixture_experts_layer_24_b200 import train
+    calls = []
+    for mod in (B, train):
+        for name in CALLS:
+            if hasattr(mod, name):
+                monkeypatch.setattr(mod, name, lambda *a, _n=name, **k: calls.append(_n))
+        monkeypatch.setattr(mod, "moe_workspace_size", lambda ctx, T: 4096)
+    monkeypatch.setattr(B, "moe_route_bwd_workspace_size", lambda ctx, T: 64)
+    L = object.__new__(B.MoeLayer)
+    L.H, L.E, L.K, L.I, L.wdtype = 256, 8, 2, 128, B.MOE_BF16
+    L.device, L.ctx, L.slots, L._keep, L._ws = torch.device("cpu"), None, None, {}, None
+    return L, calls
+
+
+def _args(T=5):
+    H, E, K, I = 256, 8, 2, 128
+    z = torch.zeros
+    bf, i32 = torch.bfloat16, torch.int32
+    return dict(x=z((T, H), dtype=bf), rows=z((T * K, H), dtype=bf), inv=z((T, K), dtype=i32),
+                idx=z((T, K), dtype=i32), w=z((T, K)), wr=z((E, H)), offsets=z((E + 1,), dtype=i32),
+                perm=z((T * K,), dtype=i32), gu=z((T * K, 2 * I), dtype=bf), dh=z((T * K, I), dtype=bf),
+                q=z((T * K, 2 * I), dtype=torch.uint8), s=z((T * K, 2 * I // 128)),
+                w_gu=z((E, 2 * I, H), dtype=bf), w_dn=z((E, H, I), dtype=bf))
+
+
+def test_layer_methods_take_valid_arguments(host_layer):
+    L, calls = host_layer
+    for T in (5, 0):
+        a = _args(T)
+        assert L.dispatch(a["x"], a["inv"]).shape == (2 * T, 256)
+        assert L.dispatch(a["x"].float(), a["inv"]).dtype == torch.float32
+        assert L.dispatch(a["x"].to(torch.uint8), a["inv"], x_scales=torch.zeros(T, 2)).dtype == torch.bfloat16
+        assert L.dispatch_bwd(a["rows"], a["inv"]).shape == (T, 256)
+        assert L.dispatch_bwd(a["rows"], a["inv"], a["w"], a["idx"], a["wr"], out=a["x"]) is a["x"]
+        assert L.combine_weighted(a["rows"].float(), a["w"], a["inv"]).dtype == torch.float32
+        dy, dw = L.combine_weighted_bwd(a["x"], a["rows"], a["w"], a["inv"])
+        assert dy.shape == (2 * T, 256) and dw.shape == (T, 2)
+        h, q, s = L.swiglu_ckpt(a["gu"], a["inv"])
+        assert h.shape == (2 * T, 128) and q.shape == (2 * T, 256) and s.shape == (2 * T, 2)
+        dgu, hw, dw = L.swiglu_ckpt_bwd(a["q"], a["s"], a["dh"], topk_w=a["w"], inv=a["inv"])
+        assert dgu.shape == (2 * T, 256) and hw.shape == (2 * T, 128) and dw.shape == (T, 2)
+        assert L.swiglu_ckpt_bwd(a["q"], a["s"], a["dh"])[1:] == (None, None)
+        dl, dwr, db = L.route_bwd(a["x"], a["w"], a["w"], a["offsets"], a["perm"], a["perm"])
+        assert dl.shape == (T, 2) and dwr.shape == (8, 256) and db.shape == (8,)
+        assert L.expert_product(a["rows"], a["w_gu"], a["offsets"]).shape == (2 * T, 256)
+        assert L.expert_product(a["rows"], a["w_dn"], a["offsets"], transposed=True).shape == (2 * T, 128)
+        assert L.expert_wgrad(a["gu"], a["rows"], a["offsets"], dtype=torch.float32).shape == (8, 256, 256)
+    L.swiglu_ckpt(torch.zeros((3, 256), dtype=torch.bfloat16))  # rows that are no whole number of tokens, without inv
+    assert len(set(calls)) == 9
+
+
+def test_layer_methods_refuse_bad_arguments_before_any_call(host_layer):
+    L, calls = host_layer
+    a = _args()
+    half = torch.float16
+    bad = [
+        lambda: L.dispatch(a["x"].to(half), a["inv"]),
+        lambda: L.dispatch(a["x"], a["inv"].long()),
+        lambda: L.dispatch(a["x"], a["inv"][:, :1].contiguous()),
+        lambda: L.dispatch(a["x"][:, :128], a["inv"]),
+        lambda: L.dispatch(a["x"], a["inv"], x_scales=torch.zeros(5, 2)),             # bf16 rows with scales
+        lambda: L.dispatch(a["x"].to(torch.uint8), a["inv"]),                         # codes without scales
+        lambda: L.dispatch(a["x"].to(torch.uint8), a["inv"], x_scales=torch.zeros(5, 1)),
+        lambda: L.dispatch(a["x"], a["inv"], out=a["x"]),
+        lambda: L.dispatch_bwd(a["rows"][:-1], a["inv"]),
+        lambda: L.dispatch_bwd(a["rows"].t().contiguous().t(), a["inv"]),              # not row-major
+        lambda: L.dispatch_bwd(a["rows"], a["inv"], dlogit=a["w"]),                   # the router's three go together
+        lambda: L.dispatch_bwd(a["rows"], a["inv"], a["w"], a["idx"], a["wr"][:4]),
+        lambda: L.combine_weighted(a["rows"], a["w"].double(), a["inv"]),
+        lambda: L.combine_weighted(a["rows"], a["w"], a["inv"], out=a["x"].float()),
+        lambda: L.combine_weighted_bwd(a["x"].float(), a["rows"], a["w"], a["inv"]),   # two row types
+        lambda: L.swiglu_ckpt(a["gu"].float(), a["inv"]),
+        lambda: L.swiglu_ckpt(a["gu"][:-1].contiguous(), a["inv"]),
+        lambda: L.swiglu_ckpt(a["dh"], a["inv"]),
+        lambda: L.swiglu_ckpt_bwd(a["q"].to(torch.int8), a["s"], a["dh"]),
+        lambda: L.swiglu_ckpt_bwd(a["q"], a["s"][:, :1].contiguous(), a["dh"]),
+        lambda: L.swiglu_ckpt_bwd(a["q"], a["s"], a["dh"], topk_w=a["w"][:2]),
+        lambda: L.swiglu_ckpt_bwd(a["q"], a["s"], a["dh"], out=(a["gu"], a["dh"])),   # hw without weights
+        lambda: L.route_bwd(a["x"].float(), a["w"], a["w"], a["offsets"], a["perm"], a["perm"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], a["offsets"][:-1], a["perm"], a["perm"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], a["offsets"], a["perm"][:-1], a["perm"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], a["offsets"], a["perm"], a["perm"], x_scales=torch.zeros(5, 2)),
+        lambda: L.expert_product(a["rows"], a["w_gu"][:4], a["offsets"]),
+        lambda: L.expert_product(a["rows"], a["w_gu"][0], a["offsets"]),
+        lambda: L.expert_product(a["rows"], a["w_dn"], a["offsets"]),                  # K does not match
+        lambda: L.expert_product(a["rows"].float(), a["w_gu"], a["offsets"]),
+        lambda: L.expert_wgrad(a["gu"], a["rows"][:-1], a["offsets"]),
+        lambda: L.expert_wgrad(a["gu"], a["rows"], a["offsets"], dtype=half),
+        lambda: L.expert_wgrad(a["gu"], a["rows"], a["offsets"], accumulate=True),     # nothing to add to
+        lambda: L.expert_wgrad(a["gu"], a["rows"], a["offsets"], out=torch.zeros(8, 256, 128)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+        assert not calls, f"bad call {i} reached the C ABI"
+
+
+def test_train_step_order_of_calls(host_layer):
+    from mixture_experts_layer_24_b200 import train
+    L, calls = host_layer
+    a = _args()
+    out, saved = train.forward(L, a["x"], a["wr"], a["w_gu"], a["w_dn"], ckpt_x=True)
+    assert out.shape == a["x"].shape and saved.x.dtype == torch.uint8
+    g = train.backward(L, saved, a["x"], a["wr"], a["w_gu"], a["w_dn"], w_dtype=torch.float32)
+    assert g.w_gu.shape == a["w_gu"].shape and g.w_dn.shape == a["w_dn"].shape and g.w_gu.dtype == torch.float32
+    assert calls == ["moe_route", "moe_permute", "moe_dispatch", "moe_expert_product", "moe_swiglu_ckpt",
+                     "moe_expert_product", "moe_combine_weighted", "moe_quantize_e4m3", "moe_dispatch", "moe_dispatch",
+                     "moe_expert_product", "moe_swiglu_ckpt_bwd", "moe_expert_wgrad", "moe_expert_wgrad",
+                     "moe_expert_product", "moe_route_bwd", "moe_dispatch_bwd"]
+    with pytest.raises((TypeError, ValueError)):
+        train.forward(L, a["x"], a["wr"], a["w_dn"], a["w_gu"])
+
+
+def _difference(f, v, i, step=1e-6):
+    """Central difference of f at flat place i of v (float64: error about step^2 + eps/step, 1e-10 of f's scale)."""
+    keep = v.reshape(-1)[i].item()
+    v.reshape(-1)[i] = keep + step
+    up = f().item()
+    v.reshape(-1)[i] = keep - step
+    down = f().item()
+    v.reshape(-1)[i] = keep
+    return (up - down) / (2 * step)
+
+
+def test_gradient_formulas_against_differences():
+    """The formulas the kernels are held to (train_ref), chained as one backward pass, against central differences
+    of the layer's loss in 64 bits: input, router, bias and both expert weights."""
+    T, H, E, K, I = 6, 8, 5, 3, 4
+    r = R.routing(T, K, E, seed=3)
+    g = torch.Generator().manual_seed(4)
+    rnd = lambda *s: torch.randn(*s, generator=g, dtype=F64)  # noqa: E731
+    x, wr, bias, w_gu, w_dn, dout = rnd(T, H), rnd(E, H), rnd(E), rnd(E, 2 * I, H), rnd(E, H, I), rnd(T, H)
+    idx = r["idx"]
+    loss = lambda: R.layer_loss(x, wr, bias, w_gu, w_dn, dout, idx)  # noqa: E731
+    # the backward pass from the formulas
+    w = torch.softmax(torch.gather(x @ wr.t() + bias, 1, idx.long()), 1)
+    src, pk, inv, offsets = r["perm_src"].long(), r["perm_k"].long(), r["inv"], r["offsets"]
+    xs, dys = x[src], dout[src]
+    gu, _ = R.products(xs, w_gu, offsets, False)
+    dh, _ = R.products(dys, w_dn, offsets, True)
+    dg, du, h, dw_rows = R.swiglu_bwd(gu[:, :I], gu[:, I:], dh, w[src, pk])
+    dgu = torch.cat((dg, du), 1)
+    dw = dw_rows[inv.long()]
+    d_dn, _ = R.wgrads(dys, w[src, pk][:, None] * h, offsets)
+    d_gu, _ = R.wgrads(dgu, xs, offsets)
+    dxs, _ = R.products(dgu, w_gu, offsets, True)
+    dl, d_wr, d_bias = R.route_bwd(x, w, dw, idx, inv, E)[:3]
+    dx, _ = R.dispatch_bwd(dxs, inv, dl, idx, wr)
+    # the same weights' gradient through the combine
+    y, _ = R.products(h, w_dn, offsets, False)
+    assert torch.allclose(R.combine_bwd(dout, y, w, inv)[1], dw, rtol=1e-10, atol=1e-12)
+    for value, grad in ((x, dx), (wr, d_wr), (bias, d_bias), (w_gu, d_gu), (w_dn, d_dn)):
+        at = torch.randperm(value.numel(), generator=g)[:12].tolist()
+        for i in at:
+            d = _difference(loss, value, i)
+            assert abs(d - grad.reshape(-1)[i].item()) <= 1e-6 * (1 + abs(d)), i
+
+
+def test_oracle_quantiser_is_the_checkpoint_rule():
+    """The e4m3 rule of the checkpoint against its statement, and how far a decoded value may be off: half a step
+    of e4m3 relative to the value (2^-4), or of its subnormals (2^-10 of the scale), and fp32's roundings."""
+    import oracle
+    g = torch.Generator().manual_seed(7)
+    v = (torch.randn(9, 512, generator=g) * torch.logspace(-3, 3, 9)[:, None]).to(torch.bfloat16)
+    v[4, :128] = 0
+    q, s = oracle.quant_e4m3(oracle.as_u16(v), 1)
+    q, s = torch.from_numpy(q), torch.from_numpy(s)
+    back, x = R.decode(q, s), v.to(F64)
+    step = s.to(F64).repeat_interleave(128, 1)
+    assert ((back - x).abs() <= (2 ** -4 * x.abs()).maximum(2 ** -10 * step) * (1 + 2 ** -20)).all()
+    assert (s[4, 0] == 1) and (q[4, :128] == 0).all()
