@@ -49,10 +49,20 @@ constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 12
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
+constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes
+// Output staging: two store boxes per epilogue warp (weights' gradient), or
+// two pieces of 32 rows x 128 features (the other forms).
+constexpr uint32_t kStagingBytes = 8 * kStoreBox;
+constexpr uint32_t kPieceBytes = 32 * 256;
+__host__ __device__ constexpr uint32_t staging_bytes(bool wgrad) { return wgrad ? kStagingBytes : 2 * kPieceBytes; }
 
 enum Form { kForward = 0, kRowGrad = 1, kWeightGrad = 2 };
 
 // ------------------------------------------------------- cluster helpers --
+__device__ __forceinline__ void named_bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -71,35 +81,14 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 __device__ __forceinline__ void remote_arrive(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Relaxed: it publishes no data of this thread (the copies' bytes order themselves).
 __device__ __forceinline__ void remote_expect_tx(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
                "r"(bytes)
                : "memory");
-}
-
-// Bounded wait whose acquire covers the other CTA of the cluster.
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
-  }
 }
 
 // TMA load into this CTA's shared memory; the bytes complete on a barrier of
@@ -161,6 +150,24 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
          (static_cast<uint64_t>(2) << 61);
 }
 
+// TMA store of one box of this CTA's shared memory; kAdd: fp32 add in place.
+template <bool kAdd>
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int c0, int c1) {
+  if (kAdd)
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 struct Tile {
   int e, m0, row0, rows, n0, n;  // n0, n: first column and width of the N axis (weights' gradient: input features)
 };
@@ -195,14 +202,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t staging = base + kStages * kStageBytes;  // 1024-byte aligned
+  const uint32_t bars = staging + staging_bytes(kWG);
   auto full = [&](int s) { return bars + 8u * s; };  // in the leader CTA; one arrival per CTA and the bytes of both
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto landed = [&](int s) { return bars + 8u * (2 * kStages + s); };  // tail steps, before the zeros
   auto tfull = [&](int b) { return bars + 8u * (3 * kStages + b); };
   auto tempty = [&](int b) { return bars + 8u * (3 * kStages + 2 + b); };  // in the leader CTA
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kStages * kStageBytes + 8 * (3 * kStages + 4));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * kStages + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* ep_abort = reinterpret_cast<volatile int*>(tmem_slot + 2);  // written by epilogue warps only
   int* prefix = reinterpret_cast<int*>(tmem_slot + 4);  // [E + 1] N tiles before each expert (not in kWG)
 
   if (threadIdx.x == 0) {
@@ -216,6 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(tempty(b), 8);  // four epilogue warps of each CTA
     }
     *abort_flag = 0;
+    *ep_abort = 0;
     fence_mbar_init();
   }
   if (warp == 5) tmem_alloc2(smem_u32(tmem_slot), 512);
@@ -328,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // copies of the pair have landed before the leader goes on to the last cluster barrier
       if (rank == 0)
         for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
-          wait_cluster(full(g % kStages), (g / kStages) & 1);
+          mbar_wait(full(g % kStages), (g / kStages) & 1);
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
@@ -339,14 +349,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int KB = k_steps(t);
         if (KB == 0) continue;  // an expert without rows: the epilogue writes zeros
         const int buf = j & 1;
-        bool ok = j < 2 || wait_cluster(tempty(buf), ((j >> 1) - 1) & 1);
+        bool ok = j < 2 || mbar_wait(tempty(buf), ((j >> 1) - 1) & 1);
         tc_fence_after();
         const uint32_t d = tmem + buf * kTileN;
         const uint32_t idesc =
             instr_desc(256, t.n, 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
         for (int kb = 0; ok && kb < KB; ++kb, ++consumed) {
           const int s = consumed % kStages;
-          if (!wait_cluster(full(s), (consumed / kStages) & 1)) {
+          if (!mbar_wait(full(s), (consumed / kStages) & 1)) {
             ok = false;
             break;
           }
@@ -407,18 +417,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    int j = 0;
+    int j = 0, piece = 0;  // piece: staged pieces so far
     for (int tile = cluster; tile < total; tile += n_clusters) {
       const Tile t = decode(tile);
       const int KB = k_steps(t);
-      const int f = t.m0 + (int)rank * 128 + warp * 32 + lane;  // this lane's feature (M axis)
       const bool in_m = t.m0 + (int)rank * 128 < a.m_total;     // CTA-uniform
       const int buf = j & 1;
       if (KB > 0) {
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(tfull(buf), (j >> 1) & 1) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
+        if (lane == 0 && !mbar_wait(tfull(buf), (j >> 1) & 1)) *ep_abort = 1;
+        named_bar_sync(2, 128);  // the four warps leave the loop together or not at all
+        if (*ep_abort) {
           if (lane == 0) {
             *abort_flag = 1;
             flag_status(a.status, MOE_DEV_TIMEOUT);
@@ -430,49 +438,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (in_m) {
         const uint32_t tl = tmem + buf * kTileN + (static_cast<uint32_t>(warp * 32) << 16);
         const int cols = kWG ? t.n : t.rows;
+        // columns per step: a 128-byte store box of the output type, or 32 rows of the output
+        const int step = kWG && !a.out_f32 ? 64 : 32;
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
+        for (int c = 0; c < cols; c += step, ++piece) {
           uint32_t v[32];
-          if (KB > 0) {
-            tmem_ld32(tl + c, v);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = 0u;
-          }
-          if (kWG) {
-            const size_t at = ((size_t)t.e * a.m_total + f) * a.n_total + t.n0 + c;
-            if (a.out_f32) {
-              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                float4 w = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                       __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-                if (a.accumulate) {
-                  const float4 old = o[q];
-                  w.x += old.x, w.y += old.y, w.z += old.z, w.w += old.w;
-                }
-                o[q] = w;
-              }
+          auto load = [&](int at) {
+            if (KB > 0) {
+              tmem_ld32(tl + at, v);
+              tmem_wait_ld();
             } else {
-              uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
+              for (int q = 0; q < 32; ++q) v[q] = 0u;
+            }
+          };
+          if (kWG) {
+            // this lane's 128-byte row of the box, 16-byte chunks swizzled as the store expects them
+            const uint32_t at = staging + (warp * 2 + (piece & 1)) * kStoreBox;
+            uint8_t* row = gbase + (at - base) + lane * 128;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box is free again
+            __syncwarp();
+            if (a.out_f32) {
+              load(c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * i]),
-                                                                  __uint_as_float(v[8 * q + 2 * i + 1]));
-                  w[i] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) =
+                    make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            } else {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                load(c + half * 32);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  *reinterpret_cast<uint4*>(row + (((half * 4 + q) ^ (lane & 7)) << 4)) =
+                      make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                                 pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
               }
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              const int r = t.e * a.m_total + t.m0 + (int)rank * 128 + warp * 32;
+              if (a.accumulate) tma_store_2d<true>(&maps.out, at, t.n0 + c, r);
+              else tma_store_2d<false>(&maps.out, at, t.n0 + c, r);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
           } else {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)(t.row0 + c) * a.m_total + f;
+            // The accumulator holds features in lanes and rows in columns: the four warps turn 32 rows x 128
+            // features round in shared memory, then write whole 256-byte pieces of each row (64-byte pieces
+            // straight from the lanes took three times as long at K = 512).
+            uint8_t* buf32 = gbase + (staging - base) + (piece & 1) * kPieceBytes;
+            load(c);
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-              if (c + q < cols) out[(size_t)q * a.m_total] = __float2bfloat16_rn(__uint_as_float(v[q]));
+              *reinterpret_cast<__nv_bfloat16*>(buf32 + q * 256 + (warp * 32 + lane) * 2) =
+                  __float2bfloat16_rn(__uint_as_float(v[q]));
+            named_bar_sync(1, 128);  // also: everyone is done reading the piece before last
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t.m0 + rank * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q = warp * 8 + i * 2 + (lane >> 4), ch = lane & 15;
+              if (c + q < cols)
+                *reinterpret_cast<uint4*>(out + (size_t)(t.row0 + c + q) * a.m_total + ch * 8) =
+                    *reinterpret_cast<const uint4*>(buf32 + q * 256 + ch * 16);
+            }
           }
         }
       }
@@ -483,6 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++j;
       }
     }
+    // the stores have read their boxes and reached global memory before the CTA goes
+    if (kWG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -497,7 +528,9 @@ namespace {
 template <int FORM>
 cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long max_tiles, int num_sms,
                         cudaStream_t s) {
-  const size_t smem = 1024 + (size_t)kStages * kStageBytes + 8 * (3 * kStages + 4) + 16 + 4 * (a.E + 1);
+  constexpr bool kWG = FORM == kWeightGrad;
+  const size_t smem = 1024 + (size_t)kStages * kStageBytes + staging_bytes(kWG) + 8 * (3 * kStages + 4) + 16 +
+                      (kWG ? 0 : 4 * ((size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
   const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

@@ -305,11 +305,12 @@ cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w,
                              const int32_t* perm_src, const int32_t* perm_k, int T, int K, int E, int H, float* dl,
                              float* dwr, float* dbias, float* ws, int* status, cudaStream_t s);
 
-// Tensor maps of one expert product: the M operand (weights, or dy) and the N
-// operand (rows); the K-major N operand has one map per box height 16 << i.
+// Tensor maps of one expert product: the M operand (weights, or dy), the N
+// operand (rows) and the output of the weights' gradient; the K-major N operand has one map per box height 16 << i.
 struct alignas(64) ProductMaps {
   CUtensorMap m;
   CUtensorMap n[4];
+  CUtensorMap out;  // weights' gradient: boxes of 32 rows x 128 bytes
 };
 
 struct ProductArgs {

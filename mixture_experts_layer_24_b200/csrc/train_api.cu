@@ -67,14 +67,14 @@ moe_status_t check_features(int n_in, int n_out) {
   return MOE_OK;
 }
 
-// bf16 [rows, inner] with boxes of 64 elements x box_rows rows, 128-byte swizzle.
+// bf16 or fp32 [rows, inner] with boxes of 128 bytes x box_rows rows, 128-byte swizzle.
 moe_status_t encode(const moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
-                    uint32_t box_rows) {
+                    uint32_t box_rows, bool f32 = false) {
   const cuuint64_t dims[2] = {inner, rows};
-  const cuuint64_t strides[1] = {inner * 2};
-  const cuuint32_t box[2] = {64u, box_rows};
+  const cuuint64_t strides[1] = {inner * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = ctx->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+  const CUresult r = ctx->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
                                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
@@ -248,6 +248,7 @@ moe_status_t moe_expert_product(moe_ctx_t* ctx, const void* a, const void* w, co
   ProductMaps maps;
   if ((st = encode(ctx, &maps.m, w, n_in, (uint64_t)E * n_out, transposed ? 64 : 128)) != MOE_OK) return st;
   if ((st = encode_rows(ctx, &maps, a, k, P)) != MOE_OK) return st;
+  maps.out = maps.m;  // this form writes its rows itself
   ProductArgs args{offsets, E, P, m, 0, k, out, 0, 0, ctx->d_status};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Prof p(ctx, MOE_PROF_PRODUCT, s);
@@ -276,6 +277,7 @@ moe_status_t moe_expert_wgrad(moe_ctx_t* ctx, const void* dy, const void* a, con
   if ((st = encode(ctx, &maps.m, dy, n_out, P, 64)) != MOE_OK) return st;
   if ((st = encode(ctx, &maps.n[0], a, n_in, P, 64)) != MOE_OK) return st;
   for (int i = 1; i < 4; ++i) maps.n[i] = maps.n[0];
+  if ((st = encode(ctx, &maps.out, dw, n_in, (uint64_t)E * n_out, 32, dtype == MOE_T_F32)) != MOE_OK) return st;
   ProductArgs args{offsets, E, P, n_out, n_in, 0, dw, dtype == MOE_T_F32, accumulate, ctx->d_status};
   Prof p(ctx, MOE_PROF_PRODUCT, s);
   MOE_CUDA(launch_expert_product(2, maps, args, ctx->num_sms, s));
