@@ -172,17 +172,19 @@ struct Tile {
   int e, m0, row0, rows, n0, n;  // n0, n: first column and width of the N axis (weights' gradient: input features)
 };
 
-// Rows of expert e, clamped so that a bad offsets entry never leads outside [0, P).
-__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int P, int& row0, int& rows,
-                                            int* status) {
-  const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
-  if (a < 0 || b < a || b > P) {
+// The sorted rows [begin, end) of one expert as `offsets` has them.
+struct Rows {
+  int begin, end;
+  // No rows in place of a range that is not inside [0, P].
+  __device__ Rows within(int P, int* status) const {
+    if (begin >= 0 && end >= begin && end <= P) return *this;
     flag_status(status, MOE_DEV_BAD_INDEX);
-    row0 = rows = 0;
-    return;
+    return Rows{0, 0};
   }
-  row0 = a;
-  rows = b - a;
+};
+
+__device__ __forceinline__ Rows expert_rows(const int32_t* __restrict__ offsets, int e) {
+  return Rows{__ldg(offsets + e), __ldg(offsets + e + 1)};
 }
 
 }  // namespace
@@ -212,7 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * kStages + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* ep_abort = reinterpret_cast<volatile int*>(tmem_slot + 2);  // written by epilogue warps only
-  int* prefix = reinterpret_cast<int*>(tmem_slot + 4);  // [E + 1] N tiles before each expert (not in kWG)
+  // not in kWG: [E + 1] N tiles before each expert, [E] its first row, [E] its rows
+  int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
+  int *first_row = prefix + a.E + 1, *n_rows = first_row + a.E;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -234,9 +238,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       int nt = 0;
       if (e0 + lane < a.E) {
-        int r0, rows;
-        expert_rows(a.offsets, e0 + lane, a.P, r0, rows, a.status);
-        nt = (rows + kTileN - 1) / kTileN;
+        const Rows r = expert_rows(a.offsets, e0 + lane).within(a.P, a.status);
+        first_row[e0 + lane] = r.begin;
+        n_rows[e0 + lane] = r.end - r.begin;
+        nt = (r.end - r.begin + kTileN - 1) / kTileN;
       }
       int incl = nt;
 #pragma unroll
@@ -257,16 +262,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const int n_tiles_w = (a.n_total + kTileN - 1) / kTileN;  // kWG: N tiles of one expert
   const int total = kWG ? a.E * m_tiles * n_tiles_w : prefix[a.E] * m_tiles;
-  auto decode = [&](int tile) {
+  // kWG: the raw rows of a tile's expert are read one tile ahead, so that no role waits for them between tiles.
+  const int per_expert = m_tiles * n_tiles_w;
+  auto ahead = [&](int tile) { return kWG && tile < total ? expert_rows(a.offsets, tile / per_expert) : Rows{0, 0}; };
+  auto decode = [&](int tile, const Rows& raw) {
     Tile t;
     if (kWG) {
-      const int per = m_tiles * n_tiles_w;
-      t.e = tile / per;
-      const int r = tile - t.e * per;
+      t.e = tile / per_expert;
+      const int r = tile - t.e * per_expert;
       t.m0 = (r / n_tiles_w) * kTileM;
       t.n0 = (r % n_tiles_w) * kTileN;
       t.n = min(kTileN, a.n_total - t.n0);
-      expert_rows(a.offsets, t.e, a.P, t.row0, t.rows, nullptr);
+      const Rows rows = raw.within(a.P, a.status);
+      t.row0 = rows.begin;
+      t.rows = rows.end - rows.begin;
     } else {
       int lo = 0, hi = a.E;
       while (hi - lo > 1) {
@@ -276,13 +285,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const int nti = prefix[lo + 1] - prefix[lo];
       const int r = tile - prefix[lo] * m_tiles;
-      int row0, rows;
-      expert_rows(a.offsets, lo, a.P, row0, rows, nullptr);
+      const int nt = r % nti;
       t.e = lo;
       t.m0 = (r / nti) * kTileM;
-      const int nt = r % nti;
-      t.row0 = row0 + nt * kTileN;
-      t.rows = min(kTileN, rows - nt * kTileN);
+      t.row0 = first_row[lo] + nt * kTileN;
+      t.rows = min(kTileN, n_rows[lo] - nt * kTileN);
       t.n0 = 0;
       t.n = (t.rows + 31) & ~31;
     }
@@ -294,8 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       int issued = 0;
+      Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total && !*abort_flag; tile += n_clusters) {
-        const Tile t = decode(tile);
+        const Tile t = decode(tile, raw);
+        raw = ahead(tile + n_clusters);
         const int KB = k_steps(t);
         const int half = t.n / 2;  // this CTA's part of the N operand
         const int mrow = t.m0 + (int)rank * 128;
@@ -344,8 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0 && lane == 0) {
       int consumed = 0, j = 0;
+      Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total; tile += n_clusters) {
-        const Tile t = decode(tile);
+        const Tile t = decode(tile, raw);
+        raw = ahead(tile + n_clusters);
         const int KB = k_steps(t);
         if (KB == 0) continue;  // an expert without rows: the epilogue writes zeros
         const int buf = j & 1;
@@ -386,8 +397,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (kWG) {
       int before = 0;
       uint32_t phases = 0;  // bit s: parity of the next use of landed(s)
+      Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total; tile += n_clusters) {
-        const Tile t = decode(tile);
+        const Tile t = decode(tile, raw);
+        raw = ahead(tile + n_clusters);
         const int KB = k_steps(t);
         before += KB;
         const int rem = t.rows & 63;
@@ -418,8 +431,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------------- epilogue
     int j = 0, piece = 0;  // piece: staged pieces so far
+    Rows raw = ahead(cluster);
     for (int tile = cluster; tile < total; tile += n_clusters) {
-      const Tile t = decode(tile);
+      const Tile t = decode(tile, raw);
+      raw = ahead(tile + n_clusters);
       const int KB = k_steps(t);
       const bool in_m = t.m0 + (int)rank * 128 < a.m_total;     // CTA-uniform
       const int buf = j & 1;
@@ -530,7 +545,7 @@ cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long
                         cudaStream_t s) {
   constexpr bool kWG = FORM == kWeightGrad;
   const size_t smem = 1024 + (size_t)kStages * kStageBytes + staging_bytes(kWG) + 8 * (3 * kStages + 4) + 16 +
-                      (kWG ? 0 : 4 * ((size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
+                      (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
   const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
