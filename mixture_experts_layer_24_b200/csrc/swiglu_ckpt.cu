@@ -17,7 +17,11 @@
 //
 // Bound by HBM: 10 bytes per (row, column of I) each way. A half-warp owns a
 // 128-column block: 16 lanes x 8 values, so that every access is 8 or 16 bytes
-// and a block's amax needs four shuffles.
+// and a block's amax needs four shuffles. What stood in the way was arithmetic:
+// IEEE divisions (one per code, one per sigmoid). Codes now take a reciprocal
+// per block and three fused multiply-adds per value, to the same bits (below);
+// the sigmoid takes the fast exponential and division, whose error (at most
+// (2 + 1.2 |g|) 2^-23, and 2^-22) is far below the bf16 rounding that follows.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -25,24 +29,52 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// Where exp(-g) passes 2^126 the division gives 0 for a true value below 2^-126.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-// amax over the 16 lanes that share a 128-column block; NaN values do not count.
-__device__ __forceinline__ float block_amax(const float (&f)[8]) {
-  float m = 0.0f;
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
+// The largest magnitudes of 8 g (low half) and 8 u (high half) values of this lane, then over the 16 lanes that
+// share a 128-column block: whole in bf16, two at a time. NaN values do not count.
+__device__ __forceinline__ float2 block_amax(const uint4& g, const uint4& u) {
+  const __nv_bfloat162 mg = __hmax2(__hmax2(__habs2(as_bf162(g.x)), __habs2(as_bf162(g.y))),
+                                    __hmax2(__habs2(as_bf162(g.z)), __habs2(as_bf162(g.w))));
+  const __nv_bfloat162 mu = __hmax2(__hmax2(__habs2(as_bf162(u.x)), __habs2(as_bf162(u.y))),
+                                    __hmax2(__habs2(as_bf162(u.z)), __habs2(as_bf162(u.w))));
+  __nv_bfloat162 m = __hmax2(__lows2bfloat162(mg, mu), __highs2bfloat162(mg, mu));
+  m = __hmax2(m, __floats2bfloat162_rn(0.0f, 0.0f));
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  for (int o = 8; o >= 1; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return __bfloat1622float2(m);
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float s) {
-  uint32_t w[2] = {0u, 0u};
+// v / s rounded to nearest, as IEEE division rounds it, for a bf16 v with |v| <= amax, s = RN(amax / 448) and r the
+// fast reciprocal of s: one correction of v * r by its exact remainder.
+__device__ __forceinline__ float quotient(float v, float s, float r) {
+  const float y = v * r;
+  return fmaf(fmaf(-s, y, v), r, y);
+}
+
+// The block's scale and its codes. For 2^-50 <= amax <= 2^100 the scale and every code are those of IEEE division
+// (compared over all pairs of bf16 amax and v); other blocks divide.
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float amax, float* scale) {
+  float y[8], s;
+  if (amax >= 0x1p-50f && amax <= 0x1p100f) {
+    s = quotient(amax, 448.0f, 1.0f / 448.0f);
+    const float r = __fdividef(1.0f, s);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(f[j] / s, __NV_SATFINITE, __NV_E4M3) << (8 * (j & 3));
-  return make_uint2(w[0], w[1]);
+    for (int j = 0; j < 8; ++j) y[j] = quotient(f[j], s, r);
+  } else {
+    s = amax == 0.0f ? 1.0f : amax / 448.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = f[j] / s;
+  }
+  *scale = s;
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j], y[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // One half-warp per (row, 128-column block of I); rows are pairs in token
@@ -52,36 +84,36 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint4* __restric
                                                            uint4* __restrict__ h, uint2* __restrict__ q,
                                                            float* __restrict__ s, int* status) {
   const int l = threadIdx.x & 15;
-  const long long unit = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const long long i = unit / blocks;
+  const unsigned unit = blockIdx.x * 16u + (threadIdx.x >> 4);
+  const unsigned i = unit / (unsigned)blocks;
   const int b = (int)(unit - i * blocks);
   int r = -1;
-  if (i < rows) r = inv ? pair_row(inv, i, rows, status) : (int)i;
+  if (i < (unsigned)rows) r = inv ? pair_row(inv, i, rows, status) : (int)i;
   const size_t gv = (size_t)(r < 0 ? 0 : r) * blocks * 32 + b * 16 + l, uv = gv + blocks * 16;  // 16-byte pieces
   uint4 ga = make_uint4(0, 0, 0, 0), ua = ga;
   if (r >= 0) {
     ga = __ldg(gu + gv);
     ua = __ldg(gu + uv);
   }
-  float g[8], u[8], o[8];
+  const float2 amax = block_amax(ga, ua);  // all lanes of the warp take part
+  if (r < 0) return;
+  float g[8], u[8], o[8], sg, su;
   RowBf16::unpack(ga, g);
   RowBf16::unpack(ua, u);
-  const float mg = block_amax(g), mu = block_amax(u);  // all lanes of the warp take part
-  if (r < 0) return;
-  const float sg = mg == 0.0f ? 1.0f : mg / 448.0f, su = mu == 0.0f ? 1.0f : mu / 448.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
   h[(size_t)r * blocks * 16 + b * 16 + l] = RowBf16::pack(o);
-  q[gv] = encode8(g, sg);
-  q[uv] = encode8(u, su);
+  q[gv] = encode8(g, amax.x, &sg);
+  q[uv] = encode8(u, amax.y, &su);
   if (l == 0) {
     s[(size_t)r * blocks * 2 + b] = sg;
     s[(size_t)r * blocks * 2 + blocks + b] = su;
   }
 }
 
-// One warp per row; each half-warp takes every second 128-column block.
-template <bool kWeighted>
+// kWarps warps per row; each half-warp takes every (2 kWarps)-th 128-column
+// block, two blocks' loads in flight.
+template <bool kWeighted, int kWarps>
 __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint2* __restrict__ q,
                                                                const float* __restrict__ s,
                                                                const uint4* __restrict__ dh,
@@ -89,43 +121,68 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint2* __res
                                                                const int32_t* __restrict__ inv, int rows, int blocks,
                                                                uint4* __restrict__ dgu, uint4* __restrict__ hw,
                                                                float* __restrict__ dw, int* status) {
-  const int lane = threadIdx.x & 31, l = lane & 15;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= rows) return;
-  const int r = inv ? pair_row(inv, i, rows, status) : (int)i;
-  if (r < 0) {
-    if (kWeighted && lane == 0) dw[i] = 0.0f;
-    return;
-  }
-  const float wk = kWeighted ? __ldg(w + i) : 1.0f;
+  constexpr int kRows = 8 / kWarps;  // rows per CTA
+  __shared__ float s_dot[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15;
+  const long long i = (long long)blockIdx.x * kRows + warp / kWarps;
+  const bool in = i < rows;
+  const int r = !in ? -1 : inv ? pair_row(inv, i, rows, status) : (int)i;
   float dot = 0.0f;
-  for (int b = lane >> 4; b < blocks; b += 2) {
-    const size_t hv = (size_t)r * blocks * 16 + b * 16 + l, gv = (size_t)r * blocks * 32 + b * 16 + l,
-                 uv = gv + blocks * 16, sv = (size_t)r * blocks * 2 + b;
-    const uint2 qg = __ldg(q + gv), qu = __ldg(q + uv);
-    const uint4 dv = __ldg(dh + hv);
-    float g[8], u[8], d[8], o[8];
-    e4m3x8(qg, __ldg(s + sv), g);
-    e4m3x8(qu, __ldg(s + sv + blocks), u);
-    RowBf16::unpack(dv, d);
+  if (r >= 0) {
+    const float wk = kWeighted ? __ldg(w + i) : 1.0f;
+    constexpr int kStep = 2 * kWarps;
+    for (int b0 = (warp % kWarps) * 2 + (lane >> 4); b0 < blocks; b0 += 2 * kStep) {
+      uint2 qg[2], qu[2];
+      uint4 dv[2];
+      float sg[2], su[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float sig = sigmoid(g[j]), silu = g[j] * sig, hj = silu * u[j];
-      if (kWeighted) dot = fmaf(d[j], hj, dot);
-      o[j] = wk * hj;
-      const float wd = wk * d[j];
-      const float dgj = wd * u[j] * sig * (1.0f + g[j] * (1.0f - sig));
-      u[j] = wd * silu;
-      g[j] = dgj;
+      for (int n = 0; n < 2; ++n) {
+        const int b = b0 + n * kStep;
+        if (b >= blocks) break;
+        const size_t gv = (size_t)r * blocks * 32 + b * 16 + l, sv = (size_t)r * blocks * 2 + b;
+        qg[n] = __ldg(q + gv);
+        qu[n] = __ldg(q + gv + blocks * 16);
+        dv[n] = __ldg(dh + (size_t)r * blocks * 16 + b * 16 + l);
+        sg[n] = __ldg(s + sv);
+        su[n] = __ldg(s + sv + blocks);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int b = b0 + n * kStep;
+        if (b >= blocks) break;
+        const size_t hv = (size_t)r * blocks * 16 + b * 16 + l, gv = (size_t)r * blocks * 32 + b * 16 + l;
+        float g[8], u[8], d[8], o[8];
+        e4m3x8(qg[n], sg[n], g);
+        e4m3x8(qu[n], su[n], u);
+        RowBf16::unpack(dv[n], d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float sig = sigmoid(g[j]), silu = g[j] * sig, hj = silu * u[j];
+          if (kWeighted) dot = fmaf(d[j], hj, dot);
+          o[j] = wk * hj;
+          const float wd = wk * d[j];
+          const float dgj = wd * u[j] * sig * (1.0f + g[j] * (1.0f - sig));
+          u[j] = wd * silu;
+          g[j] = dgj;
+        }
+        dgu[gv] = RowBf16::pack(g);
+        dgu[gv + blocks * 16] = RowBf16::pack(u);
+        if (kWeighted && hw) hw[hv] = RowBf16::pack(o);
+      }
     }
-    dgu[gv] = RowBf16::pack(g);
-    dgu[uv] = RowBf16::pack(u);
-    if (kWeighted && hw) hw[hv] = RowBf16::pack(o);
   }
   if (kWeighted) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) dw[i] = dot;
+    if (kWarps > 1) {  // the sums of the row's warps, in warp order
+      if (lane == 0) s_dot[warp] = dot;
+      __syncthreads();
+      const int w0 = warp / kWarps * kWarps;
+      dot = s_dot[w0];
+#pragma unroll
+      for (int n = 1; n < kWarps; ++n) dot += s_dot[w0 + n];
+    }
+    if (in && lane == 0 && warp % kWarps == 0) dw[i] = r >= 0 ? dot : 0.0f;
   }
 }
 
@@ -145,14 +202,23 @@ cudaError_t launch_swiglu_ckpt_bwd(const uint8_t* q, const float* s, const void*
                                    const int32_t* inv, int rows, int I, void* dgu, void* hw, float* dw, int* status,
                                    cudaStream_t st) {
   const int blocks = I / 128;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
   const uint2* qv = reinterpret_cast<const uint2*>(q);
   const uint4* dv = static_cast<const uint4*>(dh);
   uint4 *o = static_cast<uint4*>(dgu), *hv = static_cast<uint4*>(hw);
+  // Warps per row: as many as have a block for each half-warp, while the rows alone are too few to fill the GPU.
+  int warps = 1;
+  while (warps < 8 && 4 * warps <= blocks && rows * (long long)warps < 8192) warps *= 2;
+  const unsigned grid = (unsigned)(((long long)rows * warps + 7) / 8);
+  auto pick = [&](auto* one, auto* two, auto* four, auto* eight) {
+    (warps == 1 ? one : warps == 2 ? two : warps == 4 ? four : eight)<<<grid, 256, 0, st>>>(
+        qv, s, dv, w, inv, rows, blocks, o, hv, dw, status);
+  };
   if (w)
-    swiglu_ckpt_bwd_kernel<true><<<grid, 256, 0, st>>>(qv, s, dv, w, inv, rows, blocks, o, hv, dw, status);
+    pick(swiglu_ckpt_bwd_kernel<true, 1>, swiglu_ckpt_bwd_kernel<true, 2>, swiglu_ckpt_bwd_kernel<true, 4>,
+         swiglu_ckpt_bwd_kernel<true, 8>);
   else
-    swiglu_ckpt_bwd_kernel<false><<<grid, 256, 0, st>>>(qv, s, dv, w, inv, rows, blocks, o, hv, dw, status);
+    pick(swiglu_ckpt_bwd_kernel<false, 1>, swiglu_ckpt_bwd_kernel<false, 2>, swiglu_ckpt_bwd_kernel<false, 4>,
+         swiglu_ckpt_bwd_kernel<false, 8>);
   return cudaGetLastError();
 }
 
