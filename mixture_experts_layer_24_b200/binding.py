@@ -132,11 +132,10 @@ def _check(st: int, where: str):
 
 
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    """A tensor's address (an int: ctypes converts it to the declared void*), an address itself, or None."""
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr()
 
 
 def _s(stream):
@@ -145,7 +144,7 @@ def _s(stream):
             return None  # the call will fail its own checks; there is no CPU path
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
+        return stream
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -377,6 +376,13 @@ def check_tensor(t, name, dtype, shape, device=None, pinned=False):
         raise ValueError(f"{name}: host-resident weights must be in pinned memory")
 
 
+def _want(t, name, dtype, shape, device):
+    """check_tensor for the training calls: the same refusals, one expression when all is well."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        check_tensor(t, name, dtype, shape, device)
+
+
 def _rows(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D [tokens, hidden] tensor")
@@ -521,82 +527,102 @@ class MoeLayer:
         if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=self.device)
+            if stream.device != self.device:
+                raise ValueError(f"stream: of {stream.device}, expected one of {self.device}")
             return torch.cuda.stream(stream)
-        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
+        return torch.cuda.device(self.device) if self._elsewhere(None) else contextlib.nullcontext()
+
+    def _elsewhere(self, stream):
+        """Whether a call has to leave the current stream or device first."""
+        if stream is not None:
+            return True
+        return self.device.type == "cuda" and torch.cuda.current_device() != self.device.index
+
+    def _stream(self):
+        """The handle of the current stream of this layer's device, which is the current one here."""
+        if self.device.type != "cuda":
+            return None  # the call will fail its own checks; there is no CPU path
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def _out(self, t, name, dtype, shape):
         """The caller's output tensor, checked, or a new one."""
         if t is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        check_tensor(t, name, dtype, shape, self.device)
+        _want(t, name, dtype, shape, self.device)
         return t
 
     def dispatch(self, x, inv, x_scales=None, out=None, stream=None):
         """Tokens in expert order, [T*K, H]: row inv[t, k] is x[t]. x is bf16 or fp32, or the e4m3 codes (uint8) of a
         checkpoint with x_scales [T, H/128], which come back as bf16. Rows that no pair names are not written."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.dispatch(x, inv, x_scales, out)
         T = _rows(x, "x")
         if x_scales is None:
             kind, dtype = _row_type(x, "x"), x.dtype
         else:
             kind, dtype = MOE_T_E4M3_B128, torch.bfloat16
-            check_tensor(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
-        check_tensor(x, "x", x.dtype if x_scales is None else torch.uint8, (T, self.H), self.device)
-        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
-        with self._on(stream):
-            out = self._out(out, "out", dtype, (T * self.K, self.H))
-            moe_dispatch(self.ctx, x, x_scales, kind, inv, T, out)
+            _want(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
+        _want(x, "x", x.dtype if x_scales is None else torch.uint8, (T, self.H), self.device)
+        _want(inv, "inv", torch.int32, (T, self.K), self.device)
+        out = self._out(out, "out", dtype, (T * self.K, self.H))
+        moe_dispatch(self.ctx, x, x_scales, kind, inv, T, out, self._stream())
         return out
 
     def dispatch_bwd(self, dx_sorted, inv, dlogit=None, topk_idx=None, w_router=None, out=None, stream=None):
         """dx [T, H]: each token's rows of dx_sorted [T*K, H] summed over k and, with dlogit [T, K] (from route_bwd),
         topk_idx and w_router, what the router's logits pass back to its input."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.dispatch_bwd(dx_sorted, inv, dlogit, topk_idx, w_router, out)
         T = _rows(inv, "inv")
         kind = _row_type(dx_sorted, "dx_sorted")
-        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
-        check_tensor(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * self.K, self.H), self.device)
+        _want(inv, "inv", torch.int32, (T, self.K), self.device)
+        _want(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * self.K, self.H), self.device)
         if dlogit is not None or topk_idx is not None or w_router is not None:
-            check_tensor(dlogit, "dlogit", torch.float32, (T, self.K), self.device)
-            check_tensor(topk_idx, "topk_idx", torch.int32, (T, self.K), self.device)
-            check_tensor(w_router, "w_router", torch.float32, (self.E, self.H), self.device)
-        with self._on(stream):
-            out = self._out(out, "out", dx_sorted.dtype, (T, self.H))
-            moe_dispatch_bwd(self.ctx, dx_sorted, kind, inv, dlogit, topk_idx, w_router, T, out)
+            _want(dlogit, "dlogit", torch.float32, (T, self.K), self.device)
+            _want(topk_idx, "topk_idx", torch.int32, (T, self.K), self.device)
+            _want(w_router, "w_router", torch.float32, (self.E, self.H), self.device)
+        out = self._out(out, "out", dx_sorted.dtype, (T, self.H))
+        moe_dispatch_bwd(self.ctx, dx_sorted, kind, inv, dlogit, topk_idx, w_router, T, out, self._stream())
         return out
 
     def combine_weighted(self, y_sorted, topk_w, inv, out=None, stream=None):
         """out [T, H] = sum over k of topk_w[t, k] * y_sorted[inv[t, k]] (bf16 or fp32 rows without their weight;
         ``combine`` takes fp32 rows that carry it)."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.combine_weighted(y_sorted, topk_w, inv, out)
         T = _rows(inv, "inv")
         kind = _row_type(y_sorted, "y_sorted")
-        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
-        check_tensor(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
-        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
-        with self._on(stream):
-            out = self._out(out, "out", y_sorted.dtype, (T, self.H))
-            moe_combine_weighted(self.ctx, y_sorted, kind, topk_w, inv, T, out)
+        _want(inv, "inv", torch.int32, (T, self.K), self.device)
+        _want(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
+        _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        out = self._out(out, "out", y_sorted.dtype, (T, self.H))
+        moe_combine_weighted(self.ctx, y_sorted, kind, topk_w, inv, T, out, self._stream())
         return out
 
     def combine_weighted_bwd(self, dout, y_sorted, topk_w, inv, out=None, stream=None):
         """(dy_sorted [T*K, H], dtopk_w [T, K]) of combine_weighted; `out` takes dy_sorted. Rows that no pair names
         are not written."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.combine_weighted_bwd(dout, y_sorted, topk_w, inv, out)
         T = _rows(inv, "inv")
         kind = _row_type(y_sorted, "y_sorted")
-        check_tensor(inv, "inv", torch.int32, (T, self.K), self.device)
-        check_tensor(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
-        check_tensor(dout, "dout", y_sorted.dtype, (T, self.H), self.device)
-        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
-        with self._on(stream):
-            out = self._out(out, "out", y_sorted.dtype, (T * self.K, self.H))
-            dw = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
-            moe_combine_weighted_bwd(self.ctx, dout, y_sorted, kind, topk_w, inv, T, out, dw)
+        _want(inv, "inv", torch.int32, (T, self.K), self.device)
+        _want(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
+        _want(dout, "dout", y_sorted.dtype, (T, self.H), self.device)
+        _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        out = self._out(out, "out", y_sorted.dtype, (T * self.K, self.H))
+        dw = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+        moe_combine_weighted_bwd(self.ctx, dout, y_sorted, kind, topk_w, inv, T, out, dw, self._stream())
         return out, dw
 
     def _pair_rows(self, t, name, inv):
         rows = _rows(t, name)
         if inv is not None:
-            check_tensor(inv, "inv", torch.int32, (rows // self.K, self.K), self.device)
+            _want(inv, "inv", torch.int32, (rows // self.K, self.K), self.device)
             if rows % self.K:
                 raise ValueError(f"{name}: {rows} rows are not a whole number of tokens of {self.K} pairs")
         return rows
@@ -605,60 +631,67 @@ class MoeLayer:
         """(h [rows, I] bf16, q [rows, 2I] uint8 e4m3 codes, s [rows, 2I/128] fp32): h = silu(g) * u of gu = [g | u]
         bf16, and the 8-bit checkpoint that swiglu_ckpt_bwd reads. With inv, rows that no pair names are left alone.
         `out` is a tuple of the three."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.swiglu_ckpt(gu, inv, out)
         rows, I = self._pair_rows(gu, "gu", inv), self.I
-        check_tensor(gu, "gu", torch.bfloat16, (rows, 2 * I), self.device)
+        _want(gu, "gu", torch.bfloat16, (rows, 2 * I), self.device)
         h, q, s = out if out is not None else (None, None, None)
-        with self._on(stream):
-            h = self._out(h, "h", torch.bfloat16, (rows, I))
-            q = self._out(q, "q", torch.uint8, (rows, 2 * I))
-            s = self._out(s, "s", torch.float32, (rows, 2 * I // 128))
-            moe_swiglu_ckpt(self.ctx, gu, inv, rows, h, q, s)
+        h = self._out(h, "h", torch.bfloat16, (rows, I))
+        q = self._out(q, "q", torch.uint8, (rows, 2 * I))
+        s = self._out(s, "s", torch.float32, (rows, 2 * I // 128))
+        moe_swiglu_ckpt(self.ctx, gu, inv, rows, h, q, s, self._stream())
         return h, q, s
 
     def swiglu_ckpt_bwd(self, q, s, dh, topk_w=None, inv=None, out=None, stream=None):
         """(dgu [rows, 2I] bf16, hw, dtopk_w) from the checkpoint (q, s) and dh [rows, I] bf16. With topk_w [T, K],
         dh is the gradient before the routing weight: dgu carries the weight, hw [rows, I] = w * h, dtopk_w [T, K] =
         <dh, h>; without, the last two are None. `out` is a tuple (dgu, hw)."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.swiglu_ckpt_bwd(q, s, dh, topk_w, inv, out)
         rows, I = self._pair_rows(dh, "dh", inv), self.I
-        check_tensor(dh, "dh", torch.bfloat16, (rows, I), self.device)
-        check_tensor(q, "q", torch.uint8, (rows, 2 * I), self.device)
-        check_tensor(s, "s", torch.float32, (rows, 2 * I // 128), self.device)
+        _want(dh, "dh", torch.bfloat16, (rows, I), self.device)
+        _want(q, "q", torch.uint8, (rows, 2 * I), self.device)
+        _want(s, "s", torch.float32, (rows, 2 * I // 128), self.device)
         if topk_w is not None:
-            check_tensor(topk_w, "topk_w", torch.float32, (rows // self.K, self.K), self.device)
+            _want(topk_w, "topk_w", torch.float32, (rows // self.K, self.K), self.device)
             if rows % self.K:
                 raise ValueError(f"dh: {rows} rows are not a whole number of tokens of {self.K} pairs")
         dgu, hw = out if out is not None else (None, None)
         dw = None
-        with self._on(stream):
-            dgu = self._out(dgu, "dgu", torch.bfloat16, (rows, 2 * I))
-            if topk_w is not None:
-                hw = self._out(hw, "hw", torch.bfloat16, (rows, I))
-                dw = torch.empty((rows // self.K, self.K), dtype=torch.float32, device=self.device)
-            elif hw is not None:
-                raise ValueError("hw: only with topk_w")
-            moe_swiglu_ckpt_bwd(self.ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dw)
+        dgu = self._out(dgu, "dgu", torch.bfloat16, (rows, 2 * I))
+        if topk_w is not None:
+            hw = self._out(hw, "hw", torch.bfloat16, (rows, I))
+            dw = torch.empty((rows // self.K, self.K), dtype=torch.float32, device=self.device)
+        elif hw is not None:
+            raise ValueError("hw: only with topk_w")
+        moe_swiglu_ckpt_bwd(self.ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dw, self._stream())
         return dgu, hw, dw
 
     def route_bwd(self, x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales=None, stream=None):
         """(dlogit [T, K], dw_router [E, H], dlogit_bias [E]), all fp32: the gradient of ``route`` through its
         weights; offsets, perm_src and perm_k are ``permute``'s. x is bf16, or the e4m3 codes (uint8) of its checkpoint
         with x_scales [T, H/128]."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.route_bwd(x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales)
         T = _rows(x, "x")
         P = T * self.K
-        check_tensor(x, "x", torch.bfloat16 if x_scales is None else torch.uint8, (T, self.H), self.device)
+        _want(x, "x", torch.bfloat16 if x_scales is None else torch.uint8, (T, self.H), self.device)
         if x_scales is not None:
-            check_tensor(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
-        check_tensor(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
-        check_tensor(dtopk_w, "dtopk_w", torch.float32, (T, self.K), self.device)
-        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
-        check_tensor(perm_src, "perm_src", torch.int32, (P,), self.device)
-        check_tensor(perm_k, "perm_k", torch.int32, (P,), self.device)
-        with self._on(stream):
-            ws = torch.empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8, device=self.device)
-            dl = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
-            dwr = torch.empty((self.E, self.H), dtype=torch.float32, device=self.device)
-            db = torch.empty((self.E,), dtype=torch.float32, device=self.device)
-            moe_route_bwd(self.ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dl, dwr, db, ws)
+            _want(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
+        _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
+        _want(dtopk_w, "dtopk_w", torch.float32, (T, self.K), self.device)
+        _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        _want(perm_src, "perm_src", torch.int32, (P,), self.device)
+        _want(perm_k, "perm_k", torch.int32, (P,), self.device)
+        ws = torch.empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8, device=self.device)
+        dl = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+        dwr = torch.empty((self.E, self.H), dtype=torch.float32, device=self.device)
+        db = torch.empty((self.E,), dtype=torch.float32, device=self.device)
+        moe_route_bwd(self.ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dl, dwr, db, ws,
+                      self._stream())
         return dl, dwr, db
 
     def _weights_shape(self, w, name):
@@ -670,34 +703,38 @@ class MoeLayer:
         """Each expert's rows of a (sorted, offsets from ``permute``) times its weights w [E, n_out, n_in] bf16:
         a [P, n_in] -> [P, n_out], or with transposed a [P, n_out] -> [P, n_in] (the gradient of the rows). Rows
         behind the last expert's are not written."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.expert_product(a, w, offsets, transposed, out)
         P = _rows(a, "a")
         n_out, n_in = self._weights_shape(w, "w")
         k, m = (n_out, n_in) if transposed else (n_in, n_out)
-        check_tensor(w, "w", torch.bfloat16, (self.E, n_out, n_in), self.device)
-        check_tensor(a, "a", torch.bfloat16, (P, k), self.device)
-        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
-        with self._on(stream):
-            out = self._out(out, "out", torch.bfloat16, (P, m))
-            moe_expert_product(self.ctx, a, w, offsets, P, n_in, n_out, transposed, out)
+        _want(w, "w", torch.bfloat16, (self.E, n_out, n_in), self.device)
+        _want(a, "a", torch.bfloat16, (P, k), self.device)
+        _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        out = self._out(out, "out", torch.bfloat16, (P, m))
+        moe_expert_product(self.ctx, a, w, offsets, P, n_in, n_out, transposed, out, self._stream())
         return out
 
     def expert_wgrad(self, dy, a, offsets, dtype=torch.bfloat16, out=None, accumulate=False, stream=None):
         """dw [E, n_out, n_in] = each expert's dy^T a over its rows (dy [P, n_out], a [P, n_in] bf16), bf16 or fp32;
         with accumulate, added to the fp32 tensor `out`."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.expert_wgrad(dy, a, offsets, dtype, out, accumulate)
         P, n_out = _rows(dy, "dy"), int(dy.shape[1])
         n_in = int(a.shape[1]) if isinstance(a, torch.Tensor) and a.dim() == 2 else -1
-        check_tensor(dy, "dy", torch.bfloat16, (P, n_out), self.device)
-        check_tensor(a, "a", torch.bfloat16, (P, n_in), self.device)
-        check_tensor(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        _want(dy, "dy", torch.bfloat16, (P, n_out), self.device)
+        _want(a, "a", torch.bfloat16, (P, n_in), self.device)
+        _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
         if out is not None:
             dtype = out.dtype
         elif accumulate:
             raise ValueError("accumulate: needs the tensor to add to (out)")
         if dtype not in _ROW_TYPES:
             raise TypeError("dtype: expected bf16 or fp32")
-        with self._on(stream):
-            out = self._out(out, "out", dtype, (self.E, n_out, n_in))
-            moe_expert_wgrad(self.ctx, dy, a, offsets, P, n_in, n_out, _ROW_TYPES[dtype], accumulate, out)
+        out = self._out(out, "out", dtype, (self.E, n_out, n_in))
+        moe_expert_wgrad(self.ctx, dy, a, offsets, P, n_in, n_out, _ROW_TYPES[dtype], accumulate, out, self._stream())
         return out
 
     def capture(self, x, w_router, logit_bias=None):

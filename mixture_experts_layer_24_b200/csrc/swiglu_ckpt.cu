@@ -15,13 +15,17 @@
 // the gradient that arrives is the unweighted dout W_dn of each pair, and the
 // down product's output need not be kept to differentiate the weight.
 //
-// Bound by HBM: 10 bytes per (row, column of I) each way. A half-warp owns a
-// 128-column block: 16 lanes x 8 values, so that every access is 8 or 16 bytes
-// and a block's amax needs four shuffles. What stood in the way was arithmetic:
-// IEEE divisions (one per code, one per sigmoid). Codes now take a reciprocal
-// per block and three fused multiply-adds per value, to the same bits (below);
-// the sigmoid takes the fast exponential and division, whose error (at most
-// (2 + 1.2 |g|) 2^-23, and 2^-22) is far below the bf16 rounding that follows.
+// Bound by HBM: 8 bytes and 10 bytes per (row, column of I). Measured at 32768
+// rows, I = 2048, of a copy's 6.56 TB/s: forward 91.7 us (90%), gradient with
+// weights 115 us (89%). What stood in the way was arithmetic: with IEEE
+// divisions (one per code, one per sigmoid) and 8 lanes' worth of shuffles the
+// forward took 166 us. Codes now take a reciprocal per block and three fused
+// multiply-adds per value, to the same bits (below); the sigmoid takes the fast
+// exponential and division, whose error (at most (2 + 1.2 |g|) 2^-23, and
+// 2^-22) is far below the bf16 rounding that follows; a block's amax is taken
+// in bf16, two values at a time, over 8 lanes of 16 values (16 lanes of 8
+// values: 109 us). The register bounds are those measured fastest: forward 48
+// (58 unbounded: 101 us), gradient 64 (74 unbounded: 121 us).
 #include "internal.h"
 #include "rows.cuh"
 
@@ -34,17 +38,19 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
-// The largest magnitudes of 8 g (low half) and 8 u (high half) values of this lane, then over the 16 lanes that
-// share a 128-column block: whole in bf16, two at a time. NaN values do not count.
-__device__ __forceinline__ float2 block_amax(const uint4& g, const uint4& u) {
-  const __nv_bfloat162 mg = __hmax2(__hmax2(__habs2(as_bf162(g.x)), __habs2(as_bf162(g.y))),
-                                    __hmax2(__habs2(as_bf162(g.z)), __habs2(as_bf162(g.w))));
-  const __nv_bfloat162 mu = __hmax2(__hmax2(__habs2(as_bf162(u.x)), __habs2(as_bf162(u.y))),
-                                    __hmax2(__habs2(as_bf162(u.z)), __habs2(as_bf162(u.w))));
+__device__ __forceinline__ __nv_bfloat162 amax8(const uint4& v) {
+  return __hmax2(__hmax2(__habs2(as_bf162(v.x)), __habs2(as_bf162(v.y))),
+                 __hmax2(__habs2(as_bf162(v.z)), __habs2(as_bf162(v.w))));
+}
+
+// The largest magnitudes of the lane's g (x) and u (y), then over the 8 lanes that share a 128-column block: whole
+// in bf16, two at a time. NaN values do not count.
+__device__ __forceinline__ float2 block_amax(const uint4 (&g)[2], const uint4 (&u)[2]) {
+  const __nv_bfloat162 mg = __hmax2(amax8(g[0]), amax8(g[1])), mu = __hmax2(amax8(u[0]), amax8(u[1]));
   __nv_bfloat162 m = __hmax2(__lows2bfloat162(mg, mu), __highs2bfloat162(mg, mu));
   m = __hmax2(m, __floats2bfloat162_rn(0.0f, 0.0f));
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 4; o >= 1; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
   return __bfloat1622float2(m);
 }
 
@@ -55,21 +61,27 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
   return fmaf(fmaf(-s, y, v), r, y);
 }
 
-// The block's scale and its codes. For 2^-50 <= amax <= 2^100 the scale and every code are those of IEEE division
-// (compared over all pairs of bf16 amax and v); other blocks divide.
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float amax, float* scale) {
-  float y[8], s;
+// The scale of a block with this amax and a factor r for its codes (0: divide). For 2^-50 <= amax <= 2^100 the scale
+// and every code below are those of IEEE division (compared over all pairs of bf16 amax and v); other blocks divide.
+__device__ __forceinline__ float block_scale(float amax, float* r) {
   if (amax >= 0x1p-50f && amax <= 0x1p100f) {
-    s = quotient(amax, 448.0f, 1.0f / 448.0f);
-    const float r = __fdividef(1.0f, s);
+    const float s = quotient(amax, 448.0f, 1.0f / 448.0f);
+    *r = __fdividef(1.0f, s);
+    return s;
+  }
+  *r = 0.0f;
+  return amax == 0.0f ? 1.0f : amax / 448.0f;
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float r) {
+  float y[8];
+  if (r != 0.0f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = quotient(f[j], s, r);
   } else {
-    s = amax == 0.0f ? 1.0f : amax / 448.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = f[j] / s;
   }
-  *scale = s;
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -77,34 +89,43 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float amax, float*
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// One half-warp per (row, 128-column block of I); rows are pairs in token
-// order (row = inv[i]) or, without inv, the rows themselves.
-__global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint4* __restrict__ gu,
+// Eight lanes per (row, 128-column block of I), 2 x 8 values of g and u each; rows are pairs in token order
+// (row = inv[i]) or, without inv, the rows themselves.
+__global__ void __launch_bounds__(256, 5) swiglu_ckpt_kernel(const uint4* __restrict__ gu,
                                                            const int32_t* __restrict__ inv, int rows, int blocks,
                                                            uint4* __restrict__ h, uint2* __restrict__ q,
                                                            float* __restrict__ s, int* status) {
-  const int l = threadIdx.x & 15;
-  const unsigned unit = blockIdx.x * 16u + (threadIdx.x >> 4);
+  const int l = threadIdx.x & 7;
+  const unsigned unit = blockIdx.x * 32u + (threadIdx.x >> 3);
   const unsigned i = unit / (unsigned)blocks;
   const int b = (int)(unit - i * blocks);
   int r = -1;
   if (i < (unsigned)rows) r = inv ? pair_row(inv, i, rows, status) : (int)i;
-  const size_t gv = (size_t)(r < 0 ? 0 : r) * blocks * 32 + b * 16 + l, uv = gv + blocks * 16;  // 16-byte pieces
-  uint4 ga = make_uint4(0, 0, 0, 0), ua = ga;
+  const size_t hv = (size_t)(r < 0 ? 0 : r) * blocks * 16 + b * 16 + l;  // 16-byte pieces of h
+  const size_t gv = (size_t)(r < 0 ? 0 : r) * blocks * 32 + b * 16 + l, uv = gv + blocks * 16;  // and of gu
+  uint4 ga[2] = {}, ua[2] = {};
   if (r >= 0) {
-    ga = __ldg(gu + gv);
-    ua = __ldg(gu + uv);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      ga[n] = __ldg(gu + gv + 8 * n);
+      ua[n] = __ldg(gu + uv + 8 * n);
+    }
   }
   const float2 amax = block_amax(ga, ua);  // all lanes of the warp take part
   if (r < 0) return;
-  float g[8], u[8], o[8], sg, su;
-  RowBf16::unpack(ga, g);
-  RowBf16::unpack(ua, u);
+  float rg, ru;
+  const float sg = block_scale(amax.x, &rg), su = block_scale(amax.y, &ru);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
-  h[(size_t)r * blocks * 16 + b * 16 + l] = RowBf16::pack(o);
-  q[gv] = encode8(g, amax.x, &sg);
-  q[uv] = encode8(u, amax.y, &su);
+  for (int n = 0; n < 2; ++n) {
+    float g[8], u[8], o[8];
+    RowBf16::unpack(ga[n], g);
+    RowBf16::unpack(ua[n], u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
+    h[hv + 8 * n] = RowBf16::pack(o);
+    q[gv + 8 * n] = encode8(g, sg, rg);
+    q[uv + 8 * n] = encode8(u, su, ru);
+  }
   if (l == 0) {
     s[(size_t)r * blocks * 2 + b] = sg;
     s[(size_t)r * blocks * 2 + blocks + b] = su;
@@ -114,7 +135,7 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint4* __restric
 // kWarps warps per row; each half-warp takes every (2 kWarps)-th 128-column
 // block, two blocks' loads in flight.
 template <bool kWeighted, int kWarps>
-__global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint2* __restrict__ q,
+__global__ void __launch_bounds__(256, 4) swiglu_ckpt_bwd_kernel(const uint2* __restrict__ q,
                                                                const float* __restrict__ s,
                                                                const uint4* __restrict__ dh,
                                                                const float* __restrict__ w,
@@ -192,7 +213,7 @@ cudaError_t launch_swiglu_ckpt(const void* gu, const int32_t* inv, int rows, int
                                int* status, cudaStream_t st) {
   const int blocks = I / 128;
   const long long units = (long long)rows * blocks;
-  swiglu_ckpt_kernel<<<(unsigned)((units + 15) / 16), 256, 0, st>>>(static_cast<const uint4*>(gu), inv, rows, blocks,
+  swiglu_ckpt_kernel<<<(unsigned)((units + 31) / 32), 256, 0, st>>>(static_cast<const uint4*>(gu), inv, rows, blocks,
                                                                      static_cast<uint4*>(h),
                                                                      reinterpret_cast<uint2*>(q), s, status);
   return cudaGetLastError();
