@@ -348,8 +348,8 @@ moe_status_t moe_dispatch(moe_ctx_t* ctx, const void* x, const float* x_scales, 
                           void* x_sorted, moe_stream_t stream);
 
 /* Gradient of the dispatch, and of the router's input where dlogit is given:
- *   dx[t, :] = sum_k dx_sorted[inv[t*K+k], :] + sum_k dlogit[t, k] * w_router[topk_idx[t, k], :]
- * k ascending in fp32 (the rows first), rounded once.
+ *   dx[t, :] = sum_k dlogit[t, k] * w_router[topk_idx[t, k], :] + sum_k dx_sorted[inv[t*K+k], :]
+ * in this order in fp32, k ascending, rounded once.
  *   dx_sorted [T*K, H], dx [T, H], both bf16 or both fp32; dlogit [T, K] fp32
  *   (moe_route_bwd), topk_idx [T, K], w_router [E, H] fp32: all three, or all
  *   NULL. A topk_idx outside [0, E) adds nothing and sets MOE_DEV_BAD_EXPERT. */

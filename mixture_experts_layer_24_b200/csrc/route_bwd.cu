@@ -7,11 +7,24 @@
 //
 // The pairs are already sorted by expert, so dWr is a segmented sum of scaled
 // rows: the sorted list is cut every `chunk` pairs, a CTA takes one piece and
-// 2048 columns, and adds up each expert's run inside it. A run that is its
+// 4096 columns, and adds up each expert's run inside it. A run that is its
 // expert's whole list is written out at once; the first and last run of a
 // piece may be parts, which go to the workspace and are added in order by a
-// second kernel (it also writes the zero rows of experts without pairs). The
-// order of every sum depends on the routing alone, so results repeat exactly.
+// second kernel. The order of every sum depends on the routing alone, so
+// results repeat exactly.
+//
+// Two launches, the second one starting under the first (programmatic
+// dependent launch): until the parts are there it writes the zero rows of
+// experts without pairs. A piece computes the dl it needs itself; CTAs behind
+// the pieces write dl out for every pair, dropped ones too.
+//
+// x is read from L2 once per pair (K times over), 268 MB for 4096 tokens of
+// 8 x 4096: 36.4 us for the two kernels, where HBM needs 6.2 us for x and dWr
+// once. What bounds it is issue: 16 columns per thread and paired fp32
+// multiply-adds (one instruction, two columns) took the pieces' kernel from 44
+// to about 28 us; more rows in flight, through registers or asynchronous
+// copies, only cost occupancy (47 to 61 us in all).
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.h"
@@ -21,189 +34,243 @@ namespace moe {
 
 namespace {
 
-constexpr int kChunkMax = 64;
-constexpr int kCols = 2048;  // columns per CTA: 256 threads x 8
+constexpr int kChunkMax = 128;
+constexpr int kMaxExperts = 1024;
 
-// dl of every pair, in token order: one thread per pair.
-__global__ void __launch_bounds__(256) route_dlogit_kernel(const float* __restrict__ w, const float* __restrict__ dw,
-                                                            int T, int K, float* __restrict__ dl) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (long long)T * K) return;
-  const long long t = i / K;
+__device__ __forceinline__ float dlogit(const float* __restrict__ w, const float* __restrict__ dw, size_t t, int k,
+                                        int K) {
   float dot = 0.0f;
-  for (int k = 0; k < K; ++k) dot = fmaf(__ldg(w + t * K + k), __ldg(dw + t * K + k), dot);
-  dl[i] = __ldg(w + i) * (__ldg(dw + i) - dot);
+  for (int j = 0; j < K; ++j) dot = fmaf(__ldg(w + t * K + j), __ldg(dw + t * K + j), dot);
+  return __ldg(w + t * K + k) * (__ldg(dw + t * K + k) - dot);
 }
 
-__device__ __forceinline__ int valid_pairs(const int32_t* __restrict__ offsets, int E, int P, int* status) {
-  const int n = __ldg(offsets + E);
-  if (n < 0 || n > P) {
-    flag_status(status, MOE_DEV_BAD_INDEX);
-    return 0;
-  }
-  return n;
+// Number of kept pairs; 0 and a report where offsets[E] is not inside [0, P].
+__device__ __forceinline__ int valid_pairs(int n, int P, int* status) {
+  if (n >= 0 && n <= P) return n;
+  flag_status(status, MOE_DEV_BAD_INDEX);
+  return 0;
 }
 
-// The expert whose rows hold sorted pair p: the last e with offsets[e] <= p.
-__device__ __forceinline__ int expert_of(const int32_t* __restrict__ offsets, int E, int p) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(offsets + mid) <= p) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+// acc (two columns) += d * f, both lanes rounded as fmaf rounds.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t d2, float lo, float hi) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%2, %3};\n\tfma.rn.f32x2 %0, %1, t, %0;\n\t}"
+      : "+l"(acc)
+      : "l"(d2), "f"(lo), "f"(hi));
 }
 
-// kCkpt: x is an e4m3 checkpoint (codes, one scale per 128 columns).
+// kCkpt: x is an e4m3 checkpoint (codes, one scale per 128 columns). A thread
+// owns 2 x 8 columns, v and v + blockDim.x in units of eight.
 template <bool kCkpt>
 __global__ void __launch_bounds__(256) route_wgrad_kernel(const void* __restrict__ x,
                                                            const float* __restrict__ scales,
-                                                           const float* __restrict__ dl,
+                                                           const float* __restrict__ w, const float* __restrict__ dw,
                                                            const int32_t* __restrict__ offsets,
                                                            const int32_t* __restrict__ perm_src,
                                                            const int32_t* __restrict__ perm_k, int T, int K, int E,
-                                                           int H, int chunk, float* __restrict__ dwr,
-                                                           float* __restrict__ dbias, float* __restrict__ part,
-                                                           float* __restrict__ part_b, int* status) {
+                                                           int H, int chunk, int pieces, float* __restrict__ dl,
+                                                           float* __restrict__ dwr, float* __restrict__ dbias,
+                                                           float* __restrict__ part, float* __restrict__ part_b,
+                                                           int* status) {
   using Piece = typename std::conditional<kCkpt, uint2, uint4>::type;  // eight columns
-  __shared__ int s_t[kChunkMax];
-  __shared__ float s_d[kChunkMax];
-  const int n = valid_pairs(offsets, E, T * K, status);
-  const int p0 = blockIdx.x * chunk, p1 = min(n, p0 + chunk);
-  if (p0 >= p1) return;
-  for (int j = threadIdx.x; j < p1 - p0; j += 256) {
-    int t = __ldg(perm_src + p0 + j);
-    const int k = __ldg(perm_k + p0 + j);
-    float d = 0.0f;
-    if (t < 0 || t >= T || k < 0 || k >= K) {
-      flag_status(status, MOE_DEV_BAD_INDEX);
-      t = -1;
-    } else {
-      d = __ldg(dl + (size_t)t * K + k);
-    }
-    s_t[j] = t;
-    s_d[j] = d;
+  __shared__ int s_off[kMaxExperts + 1];
+  __shared__ int2 s_pair[kChunkMax];  // a pair's token (-1: none) and the bits of its dl
+  __shared__ int s_e[kChunkMax];      // its expert
+  pdl_trigger();
+  const int tid = threadIdx.x, nt = blockDim.x;
+  if ((int)blockIdx.x >= pieces) {  // dl of every pair, in token order
+    const long long i = (long long)(blockIdx.x - pieces) * nt + tid;
+    if (blockIdx.y == 0 && i < (long long)T * K) dl[i] = dlogit(w, dw, i / K, (int)(i % K), K);
+    return;
+  }
+  const int p0 = blockIdx.x * chunk;
+  for (int e = tid; e <= E; e += nt) s_off[e] = __ldg(offsets + e);
+  // places behind the kept pairs may hold anything: taken as no pair, and reported below if they are not behind
+  for (int j = tid; j < min(chunk, T * K - p0); j += nt) {
+    const int t = __ldg(perm_src + p0 + j), k = __ldg(perm_k + p0 + j);
+    const bool good = t >= 0 && t < T && k >= 0 && k < K;
+    s_pair[j] = good ? make_int2(t, __float_as_int(dlogit(w, dw, t, k, K))) : make_int2(-1, 0);
   }
   __syncthreads();
+  const int n = min(valid_pairs(s_off[E], T * K, status) - p0, chunk);  // this piece's pairs
+  if (n <= 0) return;
+  bool bad = false;
+  for (int j = tid; j < n; j += nt) {
+    bad |= s_pair[j].x < 0;
+    int e = 0;  // the last expert whose rows start at or before this place
+    for (int hi = E; hi - e > 1;) {
+      const int mid = (e + hi) >> 1;
+      if (s_off[mid] <= p0 + j) e = mid;
+      else hi = mid;
+    }
+    s_e[j] = e;
+  }
+  if (bad) flag_status(status, MOE_DEV_BAD_INDEX);
+  const bool clean = !__syncthreads_or(bad);
   const int V = H / 8;
-  const int v = blockIdx.y * 256 + threadIdx.x;
-  const bool live = v < V;
-  int e = expert_of(offsets, E, p0);
-  for (int p = p0; p < p1; ++e) {
-    const int first = __ldg(offsets + e), end = __ldg(offsets + e + 1);
-    const int stop = min(p1, end);
-    float acc[8], bias = 0.0f;
+  int v[2];
+  bool live[2];
+  const Piece* xv[2];
+  const float* sv[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-    if (stop <= p) {
-      if (e >= E - 1) break;  // offsets that do not rise: nothing more to do
-      continue;
-    }
-    for (; p < stop; p += 8) {
-      Piece a[8];
-      float sc[8];
-      const int m = min(8, stop - p);
+  for (int c = 0; c < 2; ++c) {
+    v[c] = (blockIdx.y * 2 + c) * nt + tid;
+    live[c] = v[c] < V;
+    xv[c] = static_cast<const Piece*>(x) + (live[c] ? v[c] : 0);  // idle columns load too, and store nothing
+    sv[c] = kCkpt ? scales + (live[c] ? v[c] : 0) / 16 : nullptr;
+  }
+  for (int j = 0; j < n;) {
+    const int e = s_e[j];
+    const int first = s_off[e], end = s_off[e + 1];
+    // offsets that do not rise: at least this pair, so that the walk ends (the sums mean nothing then)
+    const int stop = max(j + 1, min(n, end - p0));
+    uint64_t acc[2][4] = {};
+    float bias = 0.0f;
+    auto add = [&](const Piece& a, float scale, float d, int c) {
+      float f[8];
+      if constexpr (kCkpt) e4m3x8(a, scale, f);
+      else RowBf16::unpack(a, f);
+      uint64_t d2;
+      asm("mov.b64 %0, {%1, %1};" : "=l"(d2) : "f"(d));
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        a[u] = Piece{};
-        sc[u] = 0.0f;
-        const int t = u < m ? s_t[p - p0 + u] : -1;
-        if (live && t >= 0) {
-          a[u] = __ldg(static_cast<const Piece*>(x) + (size_t)t * V + v);
-          if constexpr (kCkpt) sc[u] = __ldg(scales + (size_t)t * (V / 16) + v / 16);
+      for (int i = 0; i < 4; ++i) fma2(acc[c][i], d2, f[2 * i], f[2 * i + 1]);
+    };
+    // kRows rows in flight, then the rest of the run (and any piece with an entry to leave out) with checks
+    constexpr int kRows = 4;
+    for (; clean && j + kRows <= stop; j += kRows) {
+      Piece a[kRows][2];
+      float sc[kRows][2], d[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int2 pr = s_pair[j + u];
+        d[u] = __int_as_float(pr.y);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          a[u][c] = __ldg(xv[c] + (size_t)pr.x * V);
+          sc[u][c] = kCkpt ? __ldg(sv[c] + (size_t)pr.x * (V / 16)) : 0.0f;
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (u < m) {
-          float f[8];
-          if constexpr (kCkpt) e4m3x8(a[u], sc[u], f);
-          else RowBf16::unpack(a[u], f);
-          const float d = s_d[p - p0 + u];
+      for (int u = 0; u < kRows; ++u) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = fmaf(d, f[j], acc[j]);
-          bias += d;
-        }
+        for (int c = 0; c < 2; ++c) add(a[u][c], sc[u][c], d[u], c);
+        bias += d[u];
       }
     }
-    p = stop;
+    for (; j < stop; j += kRows) {
+      Piece a[kRows][2];
+      float sc[kRows][2];
+      int2 pr[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        pr[u] = j + u < stop ? s_pair[j + u] : make_int2(-1, 0);
+        if (pr[u].x < 0) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          a[u][c] = __ldg(xv[c] + (size_t)pr[u].x * V);
+          sc[u][c] = kCkpt ? __ldg(sv[c] + (size_t)pr[u].x * (V / 16)) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (pr[u].x < 0) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) add(a[u][c], sc[u][c], __int_as_float(pr[u].y), c);
+        bias += __int_as_float(pr[u].y);
+      }
+    }
+    j = stop;
     // whole list of e: final; otherwise a part (0: runs from the piece's first pair, 1: up to its last)
-    const bool whole = first >= p0 && end <= p1;
-    const int half = first < p0 ? 0 : 1;
-    const size_t slot = (size_t)blockIdx.x * 2 + half;
-    if (live) {
-      float4* o = reinterpret_cast<float4*>((whole ? dwr + (size_t)e * H : part + slot * H) + v * 8);
-      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    }
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    const bool whole = first >= p0 && end <= p0 + n;
+    const size_t slot = (size_t)blockIdx.x * 2 + (first < p0 ? 0 : 1);
+    float* row = whole ? dwr + (size_t)e * H : part + slot * H;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c]) {
+        ulonglong2* o = reinterpret_cast<ulonglong2*>(row + v[c] * 8);
+        o[0] = make_ulonglong2(acc[c][0], acc[c][1]);
+        o[1] = make_ulonglong2(acc[c][2], acc[c][3]);
+      }
+    if (blockIdx.y == 0 && tid == 0) {
       if (!whole) part_b[slot] = bias;
       else if (dbias) dbias[e] = bias;
     }
   }
 }
 
-// Experts whose list spans several pieces, and experts without pairs.
+// Experts whose list spans several pieces, and experts without pairs (whose
+// zeros need not wait for the pieces).
 __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __restrict__ offsets, int P, int E,
-                                                                int H, int chunk, const float* __restrict__ part,
-                                                                const float* __restrict__ part_b,
-                                                                float* __restrict__ dwr, float* __restrict__ dbias,
-                                                                int* status) {
+                                                                int H, int chunk, const float* part,
+                                                                const float* part_b, float* __restrict__ dwr,
+                                                                float* __restrict__ dbias, int* status) {
   const int e = blockIdx.x;
-  const int n = valid_pairs(offsets, E, P, status);
+  const int n = valid_pairs(__ldg(offsets + E), P, status);
   int first = __ldg(offsets + e), end = __ldg(offsets + e + 1);
   if (first < 0 || end < first || end > n) first = end = 0;
   const int b0 = first / chunk, b1 = end > first ? (end - 1) / chunk : b0;
-  if (end > first && b0 == b1) return;  // whole inside one piece: written already
+  if (end > first && b0 == b1) return;  // whole inside one piece: written there
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float bias = 0.0f;
   if (end > first) {
-    for (int b = b0; b <= b1; ++b) {
-      // the run starts inside piece b0 (its last run: slot 1), and at the start of the others (slot 0)
-      const size_t slot = (size_t)b * 2 + (b == b0 ? 1 : 0);
-      if (c < H) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(part + slot * H + c));
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    pdl_wait();
+    // the run starts inside piece b0 (its last run: slot 1), and at the start of the others (slot 0)
+    for (int b = b0; b <= b1; b += 16) {
+      float4 v[16];
+      float vb[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const size_t slot = (size_t)(b + u) * 2 + (b + u == b0 ? 1 : 0);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        vb[u] = 0.0f;
+        if (b + u <= b1 && c < H) v[u] = *reinterpret_cast<const float4*>(part + slot * H + c);
+        if (b + u <= b1 && blockIdx.y == 0) vb[u] = part_b[slot];
       }
-      bias += __ldg(part_b + slot);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        acc.x += v[u].x, acc.y += v[u].y, acc.z += v[u].z, acc.w += v[u].w;
+        bias += vb[u];
+      }
     }
   }
   if (c < H) *reinterpret_cast<float4*>(dwr + (size_t)e * H + c) = acc;
   if (dbias && blockIdx.y == 0 && threadIdx.x == 0) dbias[e] = bias;
 }
 
-}  // namespace
-
-// Pairs per piece: pieces of 64 once they fill the GPU; shorter for few pairs, where a CTA's serial walk is the time.
+// Pairs per piece: two pieces per SM. 32768 pairs of 384 experts (H = 4096): 36.4 us with two, 41.6 us with three (the
+// longest expert's parts are added in turn), 50 us with one; 8 at least, where a CTA's serial walk is the time.
 int route_bwd_chunk(int P) {
-  int c = kChunkMax;
-  while (c > 8 && P / c < 148) c >>= 1;
-  return c;
+  const int c = (P + 2 * 148 - 1) / (2 * 148);
+  return std::min(kChunkMax, std::max(8, (c + 3) / 4 * 4));
 }
+
+}  // namespace
 
 size_t route_bwd_workspace_floats(int P, int H) {
   const size_t pieces = ((size_t)P + route_bwd_chunk(P) - 1) / route_bwd_chunk(P);
   return pieces * 2 * ((size_t)H + 1);
 }
 
-cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w, const float* dw, const int32_t* offsets,
-                             const int32_t* perm_src, const int32_t* perm_k, int T, int K, int E, int H, float* dl,
-                             float* dwr, float* dbias, float* ws, int* status, cudaStream_t s) {
+cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w, const float* dw,
+                             const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T, int K,
+                             int E, int H, float* dl, float* dwr, float* dbias, float* ws, int* status, cudaStream_t s,
+                             bool pdl) {
   const int P = T * K, chunk = route_bwd_chunk(P);
-  const unsigned pieces = (unsigned)((P + chunk - 1) / chunk);
+  const int pieces = (P + chunk - 1) / chunk;
   float* part = ws;
   float* part_b = ws + (size_t)pieces * 2 * H;
   if (P > 0) {
-    route_dlogit_kernel<<<(unsigned)((P + 255) / 256), 256, 0, s>>>(w, dw, T, K, dl);
+    const int threads = std::min(256, (H / 16 + 31) / 32 * 32);
+    const dim3 grid((unsigned)(pieces + (P + threads - 1) / threads), (unsigned)((H / 16 + threads - 1) / threads));
     auto* kern = scales ? route_wgrad_kernel<true> : route_wgrad_kernel<false>;
-    kern<<<dim3(pieces, (H + kCols - 1) / kCols), 256, 0, s>>>(x, scales, dl, offsets, perm_src, perm_k, T, K, E, H,
-                                                               chunk, dwr, dbias, part, part_b, status);
+    const cudaError_t err = launch_ex(kern, grid, dim3((unsigned)threads), 0, s, false, x, scales, w, dw, offsets,
+                                      perm_src, perm_k, T, K, E, H, chunk, pieces, dl, dwr, dbias, part, part_b,
+                                      status);
+    if (err != cudaSuccess) return err;
   }
-  route_wgrad_join_kernel<<<dim3((unsigned)E, (H + 1023) / 1024), 256, 0, s>>>(offsets, P, E, H, chunk, part, part_b,
-                                                                              dwr, dbias, status);
-  return cudaGetLastError();
+  return launch_ex(route_wgrad_join_kernel, dim3((unsigned)E, (unsigned)((H + 1023) / 1024)), dim3(256), 0, s,
+                   pdl && P > 0, offsets, P, E, H, chunk, (const float*)part, (const float*)part_b, dwr, dbias,
+                   status);
 }
 
 }  // namespace moe

@@ -230,7 +230,7 @@ moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales,
   Prof p(ctx, MOE_PROF_ROUTE_BWD, s);
   ctx->launches.fetch_add(T > 0 ? kRouteBwdLaunches - 1 : 0, std::memory_order_relaxed);  // Prof counts one
   MOE_CUDA(launch_route_bwd(x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, c.top_k, c.n_experts, c.hidden, dlogit,
-                            dw_router, dlogit_bias, static_cast<float*>(ws), ctx->d_status, s));
+                            dw_router, dlogit_bias, static_cast<float*>(ws), ctx->d_status, s, ctx->chain));
   return MOE_OK;
 }
 
