@@ -23,6 +23,12 @@
 // gradient, both operands of the weights' gradient) the box is MN-major and
 // the MMA reads it transposed, so nothing is ever transposed in memory.
 //
+// An fp32 weights' gradient is summed in segments of K (kSegment), the first
+// one stored, the others added by the TMA in L2, by the same thread one after
+// the other: the tensor cores' own running sum drifts over thousands of steps.
+// A bf16 gradient is one run (its rounding, 2^-9, is larger up to a million
+// rows), and so are the other two forms (K at most 16384).
+//
 // In the weights' gradient K is the expert's own rows: the last K step of an
 // expert may hold rows of the next one (or of no expert at all, with any
 // bits in them). Those rows are zeroed in shared memory, in both operands,
@@ -48,6 +54,11 @@ constexpr int kStages = 6;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
+// K steps summed in TMEM before an fp32 gradient goes out. The tensor cores' running sum loses about 1.4e-9 of itself
+// per row: a gradient over 16384 rows summed in one run was 1.9e-5 off (2-norm), over 65536 rows 7.6e-5. In segments of
+// 14 steps (896 rows) it stays under 1e-6 for any number of rows. Time at 8192 rows, 4096 x 4096: 238 us in one run,
+// 252 us in segments of 32 steps, 272 us of 16, 326 us of 8.
+constexpr int kSegment = 14;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
 constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes
 // Output staging: two store boxes per epilogue warp (weights' gradient), or
@@ -295,6 +306,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     return t;
   };
+  // An fp32 gradient over many rows is summed in segments of at most kSegment K steps: the first is stored, the others
+  // are added in L2.
+  auto segments = [&](int KB) { return kWG && a.out_f32 && KB > kSegment ? (KB + kSegment - 1) / kSegment : 1; };
   auto k_steps = [&](const Tile& t) { return kWG ? (t.rows + 63) / 64 : a.k_total / 64; };
 
   if (warp == 4) {
@@ -359,37 +373,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         raw = ahead(tile + n_clusters);
         const int KB = k_steps(t);
         if (KB == 0) continue;  // an expert without rows: the epilogue writes zeros
-        const int buf = j & 1;
-        bool ok = j < 2 || mbar_wait(tempty(buf), ((j >> 1) - 1) & 1);
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kTileN;
+        const int nseg = segments(KB);
         const uint32_t idesc =
             instr_desc(256, t.n, 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
-        for (int kb = 0; ok && kb < KB; ++kb, ++consumed) {
-          const int s = consumed % kStages;
-          if (!mbar_wait(full(s), (consumed / kStages) & 1)) {
-            ok = false;
-            break;
-          }
+        bool ok = true;
+        for (int seg = 0; ok && seg < nseg; ++seg, ++j) {
+          const int buf = j & 1;
+          ok = j < 2 || mbar_wait(tempty(buf), ((j >> 1) - 1) & 1);
           tc_fence_after();
-          const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
-          const int left = t.rows - kb * 64;
-          const int ks = kWG ? (left >= 64 ? 4 : (left + 15) / 16) : 4;
+          const uint32_t d = tmem + buf * kTileN;
+          const int kb0 = (int)((long long)KB * seg / nseg), kb1 = (int)((long long)KB * (seg + 1) / nseg);
+          for (int kb = kb0; ok && kb < kb1; ++kb, ++consumed) {
+            const int s = consumed % kStages;
+            if (!mbar_wait(full(s), (consumed / kStages) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
+            const int left = t.rows - kb * 64;
+            const int ks = kWG ? (left >= 64 ? 4 : (left + 15) / 16) : 4;
 #pragma unroll 4
-          for (int k = 0; k < ks; ++k) {
-            const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048) : sw128_kmajor_desc(sa + k * 32);
-            const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048) : sw128_kmajor_desc(sb + k * 32);
-            mma_pair(d, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < ks; ++k) {
+              const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048) : sw128_kmajor_desc(sa + k * 32);
+              const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048) : sw128_kmajor_desc(sb + k * 32);
+              mma_pair(d, ad, bd, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
+            }
+            commit_pair(empty(s));
           }
-          commit_pair(empty(s));
+          commit_pair(tfull(buf));
         }
-        commit_pair(tfull(buf));
         if (!ok) {
           *abort_flag = 1;
           flag_status(a.status, MOE_DEV_TIMEOUT);
           break;
         }
-        ++j;
       }
     }
   } else if (warp == 6) {
@@ -431,100 +449,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------------- epilogue
     int j = 0, piece = 0;  // piece: staged pieces so far
+    bool gave_up = false;
     Rows raw = ahead(cluster);
-    for (int tile = cluster; tile < total; tile += n_clusters) {
+    for (int tile = cluster; tile < total && !gave_up; tile += n_clusters) {
       const Tile t = decode(tile, raw);
       raw = ahead(tile + n_clusters);
       const int KB = k_steps(t);
-      const bool in_m = t.m0 + (int)rank * 128 < a.m_total;     // CTA-uniform
-      const int buf = j & 1;
-      if (KB > 0) {
-        if (lane == 0 && !mbar_wait(tfull(buf), (j >> 1) & 1)) *ep_abort = 1;
-        named_bar_sync(2, 128);  // the four warps leave the loop together or not at all
-        if (*ep_abort) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            flag_status(a.status, MOE_DEV_TIMEOUT);
-          }
-          break;
-        }
-        tc_fence_after();
-      }
-      if (in_m) {
-        const uint32_t tl = tmem + buf * kTileN + (static_cast<uint32_t>(warp * 32) << 16);
-        const int cols = kWG ? t.n : t.rows;
-        // columns per step: a 128-byte store box of the output type, or 32 rows of the output
-        const int step = kWG && !a.out_f32 ? 64 : 32;
-#pragma unroll 1
-        for (int c = 0; c < cols; c += step, ++piece) {
-          uint32_t v[32];
-          auto load = [&](int at) {
-            if (KB > 0) {
-              tmem_ld32(tl + at, v);
-              tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] = 0u;
+      if (KB == 0 && a.accumulate) continue;  // nothing to add
+      const bool in_m = t.m0 + (int)rank * 128 < a.m_total;  // CTA-uniform
+      const int nseg = segments(KB);
+      for (int seg = 0; seg < nseg && !gave_up; ++seg) {
+        const int buf = j & 1;
+        if (KB > 0) {
+          if (lane == 0 && !mbar_wait(tfull(buf), (j >> 1) & 1)) *ep_abort = 1;
+          named_bar_sync(2, 128);  // the four warps leave the loop together or not at all
+          if (*ep_abort) {
+            if (lane == 0) {
+              *abort_flag = 1;
+              flag_status(a.status, MOE_DEV_TIMEOUT);
             }
-          };
-          if (kWG) {
-            // this lane's 128-byte row of the box, 16-byte chunks swizzled as the store expects them
-            const uint32_t at = staging + (warp * 2 + (piece & 1)) * kStoreBox;
-            uint8_t* row = gbase + (at - base) + lane * 128;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box is free again
-            __syncwarp();
-            if (a.out_f32) {
-              load(c);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) =
-                    make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            gave_up = true;
+            break;
+          }
+          tc_fence_after();
+        }
+        const bool add = kWG && (a.accumulate || seg > 0);
+        // what this warp stored of the last segment is in place before it adds to it
+        if (kWG && seg > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (in_m) {
+          const uint32_t tl = tmem + buf * kTileN + (static_cast<uint32_t>(warp * 32) << 16);
+          const int cols = kWG ? t.n : t.rows;
+          // columns per step: a 128-byte store box of the output type, or 32 rows of the output
+          const int step = kWG && !a.out_f32 ? 64 : 32;
+  #pragma unroll 1
+          for (int c = 0; c < cols; c += step, ++piece) {
+            uint32_t v[32];
+            auto load = [&](int at) {
+              if (KB > 0) {
+                tmem_ld32(tl + at, v);
+                tmem_wait_ld();
+              } else {
+  #pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = 0u;
+              }
+            };
+            if (kWG) {
+              // this lane's 128-byte row of the box, 16-byte chunks swizzled as the store expects them
+              const uint32_t at = staging + (warp * 2 + (piece & 1)) * kStoreBox;
+              uint8_t* row = gbase + (at - base) + lane * 128;
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box is free again
+              __syncwarp();
+              if (a.out_f32) {
+                load(c);
+  #pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) =
+                      make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              } else {
+  #pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  load(c + half * 32);
+  #pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4*>(row + (((half * 4 + q) ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                                   pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+                }
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) {
+                const int r = t.e * a.m_total + t.m0 + (int)rank * 128 + warp * 32;
+                if (add) tma_store_2d<true>(&maps.out, at, t.n0 + c, r);
+                else tma_store_2d<false>(&maps.out, at, t.n0 + c, r);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              }
             } else {
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                load(c + half * 32);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  *reinterpret_cast<uint4*>(row + (((half * 4 + q) ^ (lane & 7)) << 4)) =
-                      make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                                 pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+              // The accumulator holds features in lanes and rows in columns: the four warps turn 32 rows x 128
+              // features round in shared memory, then write whole 256-byte pieces of each row (64-byte pieces
+              // straight from the lanes took three times as long at K = 512).
+              uint8_t* buf32 = gbase + (staging - base) + (piece & 1) * kPieceBytes;
+              load(c);
+  #pragma unroll
+              for (int q = 0; q < 32; ++q)
+                *reinterpret_cast<__nv_bfloat16*>(buf32 + q * 256 + (warp * 32 + lane) * 2) =
+                    __float2bfloat16_rn(__uint_as_float(v[q]));
+              named_bar_sync(1, 128);  // also: everyone is done reading the piece before last
+              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t.m0 + rank * 128;
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int q = warp * 8 + i * 2 + (lane >> 4), ch = lane & 15;
+                if (c + q < cols)
+                  *reinterpret_cast<uint4*>(out + (size_t)(t.row0 + c + q) * a.m_total + ch * 8) =
+                      *reinterpret_cast<const uint4*>(buf32 + q * 256 + ch * 16);
               }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              const int r = t.e * a.m_total + t.m0 + (int)rank * 128 + warp * 32;
-              if (a.accumulate) tma_store_2d<true>(&maps.out, at, t.n0 + c, r);
-              else tma_store_2d<false>(&maps.out, at, t.n0 + c, r);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-          } else {
-            // The accumulator holds features in lanes and rows in columns: the four warps turn 32 rows x 128
-            // features round in shared memory, then write whole 256-byte pieces of each row (64-byte pieces
-            // straight from the lanes took three times as long at K = 512).
-            uint8_t* buf32 = gbase + (staging - base) + (piece & 1) * kPieceBytes;
-            load(c);
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              *reinterpret_cast<__nv_bfloat16*>(buf32 + q * 256 + (warp * 32 + lane) * 2) =
-                  __float2bfloat16_rn(__uint_as_float(v[q]));
-            named_bar_sync(1, 128);  // also: everyone is done reading the piece before last
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t.m0 + rank * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int q = warp * 8 + i * 2 + (lane >> 4), ch = lane & 15;
-              if (c + q < cols)
-                *reinterpret_cast<uint4*>(out + (size_t)(t.row0 + c + q) * a.m_total + ch * 8) =
-                    *reinterpret_cast<const uint4*>(buf32 + q * 256 + ch * 16);
-            }
           }
         }
-      }
-      if (KB > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
-        ++j;
+        if (KB > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
+          ++j;
+        }
       }
     }
     // the stores have read their boxes and reached global memory before the CTA goes

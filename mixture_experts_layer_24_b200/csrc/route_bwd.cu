@@ -208,12 +208,13 @@ __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __
   int first = __ldg(offsets + e), end = __ldg(offsets + e + 1);
   if (first < 0 || end < first || end > n) first = end = 0;
   const int b0 = first / chunk, b1 = end > first ? (end - 1) / chunk : b0;
+  // One CTA always waits, so that this grid is not over before the pieces' (what follows on the stream waits for it).
+  if (b1 > b0 || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
   if (end > first && b0 == b1) return;  // whole inside one piece: written there
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float bias = 0.0f;
   if (end > first) {
-    pdl_wait();
     // the run starts inside piece b0 (its last run: slot 1), and at the start of the others (slot 0)
     for (int b = b0; b <= b1; b += 16) {
       float4 v[16];

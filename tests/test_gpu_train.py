@@ -154,6 +154,7 @@ def _gate_up(seed, rows, I):
     gu = _rand(seed, rows, 2 * I, std=2.0)
     gu[0, :128] = 0                                # an all-zero block: scale 1
     gu[rows // 2, I:I + 128] *= 2.0 ** -100         # a block of tiny values
+    gu[rows // 3, I:I + 128] *= 2.0 ** -128         # and one of subnormal ones
     gu[rows - 1, 0:4] = torch.tensor([120.0, -120.0, -88.0, 30000.0], dtype=BF16)  # exp over- and underflows
     return gu
 
@@ -367,6 +368,25 @@ def test_expert_wgrad(layers, counts, slack, n_in, n_out, dtype):
             others = [i for i in range(E) if i != e]
             assert torch.equal(got[others], dw[others])
     assert L.status() == 0
+
+
+def test_wgrad_fp32_over_many_rows(layers):
+    """Positive terms, so that nothing cancels and every lost bit shows. The kernel sums 896 rows (56 steps of 16) in
+    the tensor cores and adds the segments in fp32: each of these 56 + 19 additions may lose one unit of the running
+    sum (2^-23). Summed in one run, 1024 steps, the loss was measured at 8e-5."""
+    L = layers(256, 2, 1, 128)
+    off, P = _segments([16384, 100])
+    a, dy = _rand(24, P, 256).abs(), _rand(25, P, 128).abs()
+    ref, mag = R.wgrads(dy, a, off)
+    base = torch.ones((2, 128, 256), device="cuda")
+    got = L.expert_wgrad(dy, a, off, dtype=F32)
+    _within(got, ref, (56 + 19 + 1) * 2.0 ** -23 * mag, "dw")
+    again = L.expert_wgrad(dy, a, off, dtype=F32)
+    assert torch.equal(got, again)
+    L.expert_wgrad(dy, a, off, out=base, accumulate=True)
+    _within(base, ref + 1, (56 + 19 + 2) * 2.0 ** -23 * (mag + 1), "accumulated dw")
+    half = L.expert_wgrad(dy, a, off)  # bf16: one run, one rounding
+    _within(half, ref, (1024 * 2.0 ** -23 + R.BF16_HALF) * mag * 1.01, "bf16 dw")
 
 
 def test_wgrad_without_any_row(layers):
@@ -595,6 +615,18 @@ def test_training_step_against_autograd(layers, T, H, E, K, I, ckpt_x):
     train.backward(L, saved, dout, wr, w_gu, w_dn, into=(got.w_gu, got.w_dn))
     again = train.backward(L, saved, dout, wr, w_gu, w_dn, w_dtype=F32)
     assert torch.equal(got.w_gu, 2 * again.w_gu) and torch.equal(got.w_dn, 2 * again.w_dn)
+
+
+def test_training_step_without_tokens(layers):
+    from mixture_experts_layer_24_b200 import train
+    T, H, E, K, I = 0, 256, 8, 2, 128
+    L = layers(H, E, K, I)
+    x, wr = _rand(1, T, H), _rand(2, E, H, dtype=F32)
+    w_gu, w_dn = _rand(3, E, 2 * I, H), _rand(4, E, H, I)
+    out, saved = train.forward(L, x, wr, w_gu, w_dn, ckpt_x=True)
+    g = train.backward(L, saved, out, wr, w_gu, w_dn)
+    assert out.shape == (0, H) and g.x.shape == (0, H)
+    assert all((t == 0).all() for t in (g.w_router, g.logit_bias, g.w_gu, g.w_dn)) and L.status() == 0
 
 
 def test_captured_training_step(layers):
