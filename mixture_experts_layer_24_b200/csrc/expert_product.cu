@@ -39,10 +39,23 @@
 // 5 TMEM allocation and, in the leader CTA, the MMA issuer, 6 the tail's
 // zero writer. Persistent; two TMEM accumulators of 256 columns, so a tile's
 // epilogue overlaps the next tile's MMAs. Every wait is bounded.
+//
+// Measured, 48 experts x 683 rows, 4096 x 4096 (1.1 TFLOP): forward and rows'
+// gradient 866 us cold (1270 TFLOP/s) and 900 to 1010 us under the power cap,
+// where cuBLAS' 8192^3 holds 1394; one expert x 8192 rows 192 us (1428; cuBLAS
+// 182). bf16 weights' gradient 930 to 1100 us, fp32 1060 to 1250 us (3.2 GB
+// written). 333 rows: 251 us for the 1.6 GB of weights (98% of a copy's rate).
+// What made the difference: expect_tx and waits without cluster-scope release
+// and acquire (1693 -> 916 us); whole sectors and TMA stores in the epilogue
+// (fp32 gradient 2154 -> 1207 us). What did not: bringing weights into L2
+// ahead (900 -> 995 us: the copies' issue rate is what it costs), eight
+// epilogue warps (no faster), 32-byte stores straight from the lanes (to 30%
+// slower with few rows per expert). Without its epilogue the rows' gradient
+// takes 837 us cold; the rest is the MMAs' power.
 #include <algorithm>
 
 #include "common.cuh"
-#include "internal.h"
+#include "train.h"
 
 namespace moe {
 
@@ -57,7 +70,7 @@ constexpr int kThreads = 224;
 // K steps summed in TMEM before an fp32 gradient goes out. The tensor cores' running sum loses about 1.4e-9 of itself
 // per row: a gradient over 16384 rows summed in one run was 1.9e-5 off (2-norm), over 65536 rows 7.6e-5. In segments of
 // 14 steps (896 rows) it stays under 1e-6 for any number of rows. Time at 8192 rows, 4096 x 4096: 238 us in one run,
-// 252 us in segments of 32 steps, 272 us of 16, 326 us of 8.
+// 252 us in segments of 32 steps, 272 us of 16, 286 us of 14, 326 us of 8.
 constexpr int kSegment = 14;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
 constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes

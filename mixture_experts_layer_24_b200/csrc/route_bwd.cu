@@ -27,8 +27,8 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "internal.h"
 #include "rows.cuh"
+#include "train.h"
 
 namespace moe {
 

@@ -26,8 +26,8 @@
 // in bf16, two values at a time, over 8 lanes of 16 values (16 lanes of 8
 // values: 109 us). The register bounds are those measured fastest: forward 48
 // (58 unbounded: 101 us), gradient 64 (74 unbounded: 121 us).
-#include "internal.h"
 #include "rows.cuh"
+#include "train.h"
 
 namespace moe {
 

@@ -7,7 +7,7 @@
 
 #include "../../include/moe.h"
 #include "ctx.h"
-#include "internal.h"
+#include "train.h"
 
 using namespace moe;
 

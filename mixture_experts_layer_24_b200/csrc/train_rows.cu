@@ -24,8 +24,8 @@
 // are read past L1 (they are read once), which leaves it to the router rows of
 // the busiest experts: 105 us before. A CTA that keeps 64 columns of the whole
 // router weight in shared memory and passes the tokens by it took 126 to 174 us.
-#include "internal.h"
 #include "rows.cuh"
+#include "train.h"
 
 namespace moe {
 
