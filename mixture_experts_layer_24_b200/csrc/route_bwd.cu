@@ -7,7 +7,7 @@
 //
 // The pairs are already sorted by expert, so dWr is a segmented sum of scaled
 // rows: the sorted list is cut every `chunk` pairs, a CTA takes one piece and
-// 4096 columns, and adds up each expert's run inside it. A run that is its
+// 2048 columns, and adds up each expert's run inside it. A run that is its
 // expert's whole list is written out at once; the first and last run of a
 // piece may be parts, which go to the workspace and are added in order by a
 // second kernel. The order of every sum depends on the routing alone, so
@@ -19,11 +19,12 @@
 // the pieces write dl out for every pair, dropped ones too.
 //
 // x is read from L2 once per pair (K times over), 268 MB for 4096 tokens of
-// 8 x 4096: 36.4 us for the two kernels, where HBM needs 6.2 us for x and dWr
-// once. What bounds it is issue: 16 columns per thread and paired fp32
-// multiply-adds (one instruction, two columns) took the pieces' kernel from 44
-// to about 28 us; more rows in flight, through registers or asynchronous
-// copies, only cost occupancy (47 to 61 us in all).
+// 8 x 4096: 32.3 us for the two kernels, where HBM needs 6.2 us for x and dWr
+// once. What bounds it is issue and latency together: paired fp32 multiply-adds
+// (one instruction, two columns) and four rows in flight, four blocks per SM
+// (three or five: 37 and 44 us); 16 columns per thread took 36 us, eight rows
+// in flight 42 us, rows through shared memory by asynchronous copies 54 us, and
+// a single thread's walk over the longest expert's parts 4 us more.
 #include <algorithm>
 #include <type_traits>
 
@@ -59,9 +60,9 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t d2, float lo, float
 }
 
 // kCkpt: x is an e4m3 checkpoint (codes, one scale per 128 columns). A thread
-// owns 2 x 8 columns, v and v + blockDim.x in units of eight.
+// owns eight columns.
 template <bool kCkpt>
-__global__ void __launch_bounds__(256) route_wgrad_kernel(const void* __restrict__ x,
+__global__ void __launch_bounds__(256, 4) route_wgrad_kernel(const void* __restrict__ x,
                                                            const float* __restrict__ scales,
                                                            const float* __restrict__ w, const float* __restrict__ dw,
                                                            const int32_t* __restrict__ offsets,
@@ -107,89 +108,66 @@ __global__ void __launch_bounds__(256) route_wgrad_kernel(const void* __restrict
   if (bad) flag_status(status, MOE_DEV_BAD_INDEX);
   const bool clean = !__syncthreads_or(bad);
   const int V = H / 8;
-  int v[2];
-  bool live[2];
-  const Piece* xv[2];
-  const float* sv[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    v[c] = (blockIdx.y * 2 + c) * nt + tid;
-    live[c] = v[c] < V;
-    xv[c] = static_cast<const Piece*>(x) + (live[c] ? v[c] : 0);  // idle columns load too, and store nothing
-    sv[c] = kCkpt ? scales + (live[c] ? v[c] : 0) / 16 : nullptr;
-  }
+  const int v = blockIdx.y * nt + tid;
+  const bool live = v < V;  // idle threads load too, and store nothing
+  const Piece* xv = static_cast<const Piece*>(x) + (live ? v : 0);
+  const float* sv = kCkpt ? scales + (live ? v : 0) / 16 : nullptr;
   for (int j = 0; j < n;) {
     const int e = s_e[j];
     const int first = s_off[e], end = s_off[e + 1];
     // offsets that do not rise: at least this pair, so that the walk ends (the sums mean nothing then)
     const int stop = max(j + 1, min(n, end - p0));
-    uint64_t acc[2][4] = {};
+    uint64_t acc[4] = {};
     float bias = 0.0f;
-    auto add = [&](const Piece& a, float scale, float d, int c) {
+    auto add = [&](const Piece& a, float scale, float d) {
       float f[8];
       if constexpr (kCkpt) e4m3x8(a, scale, f);
       else RowBf16::unpack(a, f);
       uint64_t d2;
       asm("mov.b64 %0, {%1, %1};" : "=l"(d2) : "f"(d));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fma2(acc[c][i], d2, f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) fma2(acc[i], d2, f[2 * i], f[2 * i + 1]);
+      bias += d;
     };
     // kRows rows in flight, then the rest of the run (and any piece with an entry to leave out) with checks
     constexpr int kRows = 4;
     for (; clean && j + kRows <= stop; j += kRows) {
-      Piece a[kRows][2];
-      float sc[kRows][2], d[kRows];
+      Piece a[kRows];
+      float sc[kRows], d[kRows];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const int2 pr = s_pair[j + u];
         d[u] = __int_as_float(pr.y);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          a[u][c] = __ldg(xv[c] + (size_t)pr.x * V);
-          sc[u][c] = kCkpt ? __ldg(sv[c] + (size_t)pr.x * (V / 16)) : 0.0f;
-        }
+        a[u] = __ldg(xv + (size_t)pr.x * V);
+        sc[u] = kCkpt ? __ldg(sv + (size_t)pr.x * (V / 16)) : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) add(a[u][c], sc[u][c], d[u], c);
-        bias += d[u];
-      }
+      for (int u = 0; u < kRows; ++u) add(a[u], sc[u], d[u]);
     }
     for (; j < stop; j += kRows) {
-      Piece a[kRows][2];
-      float sc[kRows][2];
+      Piece a[kRows];
+      float sc[kRows];
       int2 pr[kRows];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         pr[u] = j + u < stop ? s_pair[j + u] : make_int2(-1, 0);
         if (pr[u].x < 0) continue;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          a[u][c] = __ldg(xv[c] + (size_t)pr[u].x * V);
-          sc[u][c] = kCkpt ? __ldg(sv[c] + (size_t)pr[u].x * (V / 16)) : 0.0f;
-        }
+        a[u] = __ldg(xv + (size_t)pr[u].x * V);
+        sc[u] = kCkpt ? __ldg(sv + (size_t)pr[u].x * (V / 16)) : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        if (pr[u].x < 0) continue;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) add(a[u][c], sc[u][c], __int_as_float(pr[u].y), c);
-        bias += __int_as_float(pr[u].y);
-      }
+      for (int u = 0; u < kRows; ++u)
+        if (pr[u].x >= 0) add(a[u], sc[u], __int_as_float(pr[u].y));
     }
     j = stop;
     // whole list of e: final; otherwise a part (0: runs from the piece's first pair, 1: up to its last)
     const bool whole = first >= p0 && end <= p0 + n;
     const size_t slot = (size_t)blockIdx.x * 2 + (first < p0 ? 0 : 1);
-    float* row = whole ? dwr + (size_t)e * H : part + slot * H;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (live[c]) {
-        ulonglong2* o = reinterpret_cast<ulonglong2*>(row + v[c] * 8);
-        o[0] = make_ulonglong2(acc[c][0], acc[c][1]);
-        o[1] = make_ulonglong2(acc[c][2], acc[c][3]);
-      }
+    if (live) {
+      ulonglong2* o = reinterpret_cast<ulonglong2*>((whole ? dwr + (size_t)e * H : part + slot * H) + v * 8);
+      o[0] = make_ulonglong2(acc[0], acc[1]);
+      o[1] = make_ulonglong2(acc[2], acc[3]);
+    }
     if (blockIdx.y == 0 && tid == 0) {
       if (!whole) part_b[slot] = bias;
       else if (dbias) dbias[e] = bias;
@@ -198,12 +176,15 @@ __global__ void __launch_bounds__(256) route_wgrad_kernel(const void* __restrict
 }
 
 // Experts whose list spans several pieces, and experts without pairs (whose
-// zeros need not wait for the pieces).
+// zeros need not wait for the pieces). Four groups of 64 threads take a quarter
+// of the pieces each, 256 columns; their sums are added in order.
 __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __restrict__ offsets, int P, int E,
                                                                 int H, int chunk, const float* part,
                                                                 const float* part_b, float* __restrict__ dwr,
                                                                 float* __restrict__ dbias, int* status) {
-  const int e = blockIdx.x;
+  __shared__ float4 s_acc[3][64];
+  __shared__ float s_bias[3];
+  const int e = blockIdx.x, group = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int n = valid_pairs(__ldg(offsets + E), P, status);
   int first = __ldg(offsets + e), end = __ldg(offsets + e + 1);
   if (first < 0 || end < first || end > n) first = end = 0;
@@ -211,35 +192,48 @@ __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __
   // One CTA always waits, so that this grid is not over before the pieces' (what follows on the stream waits for it).
   if (b1 > b0 || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
   if (end > first && b0 == b1) return;  // whole inside one piece: written there
-  const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  const int c = (blockIdx.y * 64 + l) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float bias = 0.0f;
   if (end > first) {
     // the run starts inside piece b0 (its last run: slot 1), and at the start of the others (slot 0)
-    for (int b = b0; b <= b1; b += 16) {
-      float4 v[16];
-      float vb[16];
+    const int each = (b1 - b0 + 4) / 4, lo = b0 + group * each, hi = min(b1 + 1, lo + each);
+    for (int b = lo; b < hi; b += 8) {
+      float4 v[8];
+      float vb[8];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const size_t slot = (size_t)(b + u) * 2 + (b + u == b0 ? 1 : 0);
         v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         vb[u] = 0.0f;
-        if (b + u <= b1 && c < H) v[u] = *reinterpret_cast<const float4*>(part + slot * H + c);
-        if (b + u <= b1 && blockIdx.y == 0) vb[u] = part_b[slot];
+        if (b + u < hi && c < H) v[u] = *reinterpret_cast<const float4*>(part + slot * H + c);
+        if (b + u < hi && blockIdx.y == 0) vb[u] = part_b[slot];
       }
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
+      for (int u = 0; u < 8; ++u) {
         acc.x += v[u].x, acc.y += v[u].y, acc.z += v[u].z, acc.w += v[u].w;
         bias += vb[u];
       }
     }
   }
+  if (group > 0) {
+    s_acc[group - 1][l] = acc;
+    if (l == 0) s_bias[group - 1] = bias;
+  }
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int g = 0; g < 3; ++g) {
+    const float4 v = s_acc[g][l];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    bias += s_bias[g];
+  }
   if (c < H) *reinterpret_cast<float4*>(dwr + (size_t)e * H + c) = acc;
   if (dbias && blockIdx.y == 0 && threadIdx.x == 0) dbias[e] = bias;
 }
 
-// Pairs per piece: two pieces per SM. 32768 pairs of 384 experts (H = 4096): 36.4 us with two, 41.6 us with three (the
-// longest expert's parts are added in turn), 50 us with one; 8 at least, where a CTA's serial walk is the time.
+// Pairs per piece: two pieces per SM (32.3 us at 32768 pairs of 384 experts; three: 34.6, four: 35.5: more parts to
+// add), 8 at least (a CTA's serial walk is the time then) and 128 at most.
 int route_bwd_chunk(int P) {
   const int c = (P + 2 * 148 - 1) / (2 * 148);
   return std::min(kChunkMax, std::max(8, (c + 3) / 4 * 4));
@@ -261,15 +255,15 @@ cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w,
   float* part = ws;
   float* part_b = ws + (size_t)pieces * 2 * H;
   if (P > 0) {
-    const int threads = std::min(256, (H / 16 + 31) / 32 * 32);
-    const dim3 grid((unsigned)(pieces + (P + threads - 1) / threads), (unsigned)((H / 16 + threads - 1) / threads));
+    const int threads = std::min(256, (H / 8 + 31) / 32 * 32);
+    const dim3 grid((unsigned)(pieces + (P + threads - 1) / threads), (unsigned)((H / 8 + threads - 1) / threads));
     auto* kern = scales ? route_wgrad_kernel<true> : route_wgrad_kernel<false>;
     const cudaError_t err = launch_ex(kern, grid, dim3((unsigned)threads), 0, s, false, x, scales, w, dw, offsets,
                                       perm_src, perm_k, T, K, E, H, chunk, pieces, dl, dwr, dbias, part, part_b,
                                       status);
     if (err != cudaSuccess) return err;
   }
-  return launch_ex(route_wgrad_join_kernel, dim3((unsigned)E, (unsigned)((H + 1023) / 1024)), dim3(256), 0, s,
+  return launch_ex(route_wgrad_join_kernel, dim3((unsigned)E, (unsigned)((H + 255) / 256)), dim3(256), 0, s,
                    pdl && P > 0, offsets, P, E, H, chunk, (const float*)part, (const float*)part_b, dwr, dbias,
                    status);
 }

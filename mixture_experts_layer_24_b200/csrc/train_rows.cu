@@ -18,12 +18,13 @@
 // whole row and the token's row is shared by neighbouring warps).
 //
 // Measured at 4096 tokens, K = 8, H = 4096, bf16, of a copy's 6.56 TB/s:
-// dispatch 49 us (95%), combine 53 us (87%), its gradient 89 us (98%),
-// dispatch gradient 52 us (88%), with the router's term 70 us: that term reads
-// K fp32 router rows per token, 537 MB, which come from L1 and L2. Expert rows
-// are read past L1 (they are read once), which leaves it to the router rows of
-// the busiest experts: 105 us before. A CTA that keeps 64 columns of the whole
-// router weight in shared memory and passes the tokens by it took 126 to 174 us.
+// dispatch 49 us (95%), combine 44 us (104%: part of the rows is still in L2),
+// its gradient 89 us (98%), dispatch gradient 44 us (104%), with the router's
+// term 66 us: that term reads K fp32 router rows per token, 537 MB, which come
+// from L1 and L2. Expert rows are read past L1 (they are read once), which
+// leaves it to the router rows of the busiest experts: 105 us before. A CTA
+// that keeps 64 columns of the whole router weight in shared memory and passes
+// the tokens by it took 126 to 174 us.
 #include "rows.cuh"
 #include "train.h"
 
@@ -31,8 +32,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kSlots = 8;        // pairs whose rows are in flight per thread
-constexpr int kRouterSlots = 2;  // router rows (8: spills, 137 us; 4: 73 us; 2: 70 us at 4096 tokens of 8 x 4096)
+// Rows in flight per thread: expert rows, and router rows. Few, so that five blocks fit an SM: with eight expert rows
+// (64 registers, four blocks) the combine took 53 us and the gradient with the router's term 70 us.
+constexpr int kSlots = 4;
+constexpr int kRouterSlots = 2;
 
 // One thread per 16-byte piece of the output row.
 template <class R, bool kCkpt>
@@ -110,7 +113,7 @@ __device__ __forceinline__ void add_router(float (&acc)[kN], float d, const floa
 // kWeighted: out = sum_k w y (the combine). Otherwise the dispatch's gradient,
 // with the router's term when dl is given.
 template <class R, bool kWeighted>
-__global__ void __launch_bounds__(256, 4) gather_sum_kernel(const uint4* __restrict__ rows,
+__global__ void __launch_bounds__(256, 5) gather_sum_kernel(const uint4* __restrict__ rows,
                                                              const float* __restrict__ w,
                                                              const int32_t* __restrict__ inv,
                                                              const float* __restrict__ dl,
