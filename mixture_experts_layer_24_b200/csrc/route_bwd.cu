@@ -19,7 +19,7 @@
 // the pieces write dl out for every pair, dropped ones too.
 //
 // x is read from L2 once per pair (K times over), 268 MB for 4096 tokens of
-// 8 x 4096: 32.3 us for the two kernels, where HBM needs 6.2 us for x and dWr
+// 8 x 4096: 31.5 us for the two kernels, where HBM needs 6.2 us for x and dWr
 // once. What bounds it is issue and latency together: paired fp32 multiply-adds
 // (one instruction, two columns) and four rows in flight, four blocks per SM
 // (three or five: 37 and 44 us); 16 columns per thread took 36 us, eight rows
@@ -177,62 +177,79 @@ __global__ void __launch_bounds__(256, 4) route_wgrad_kernel(const void* __restr
 
 // Experts whose list spans several pieces, and experts without pairs (whose
 // zeros need not wait for the pieces). Four groups of 64 threads take a quarter
-// of the pieces each, 256 columns; their sums are added in order.
+// of the pieces each, kJoinVec x 256 columns (512: 2 us less than 256 or 1024);
+// their sums are added in order.
+constexpr int kJoinVec = 2;
+
 __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __restrict__ offsets, int P, int E,
                                                                 int H, int chunk, const float* part,
                                                                 const float* part_b, float* __restrict__ dwr,
                                                                 float* __restrict__ dbias, int* status) {
-  __shared__ float4 s_acc[3][64];
+  __shared__ float4 s_acc[3][kJoinVec][64];
   __shared__ float s_bias[3];
   const int e = blockIdx.x, group = threadIdx.x >> 6, l = threadIdx.x & 63;
-  const int n = valid_pairs(__ldg(offsets + E), P, status);
+  const int total = __ldg(offsets + E);
   int first = __ldg(offsets + e), end = __ldg(offsets + e + 1);
+  const int n = valid_pairs(total, P, status);
   if (first < 0 || end < first || end > n) first = end = 0;
   const int b0 = first / chunk, b1 = end > first ? (end - 1) / chunk : b0;
   // One CTA always waits, so that this grid is not over before the pieces' (what follows on the stream waits for it).
   if (b1 > b0 || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
   if (end > first && b0 == b1) return;  // whole inside one piece: written there
-  const int c = (blockIdx.y * 64 + l) * 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kJoinVec] = {};
   float bias = 0.0f;
+  auto column = [&](int i) { return ((blockIdx.y * kJoinVec + i) * 64 + l) * 4; };
   if (end > first) {
     // the run starts inside piece b0 (its last run: slot 1), and at the start of the others (slot 0)
+    constexpr int kAhead = 8 / kJoinVec;
     const int each = (b1 - b0 + 4) / 4, lo = b0 + group * each, hi = min(b1 + 1, lo + each);
-    for (int b = lo; b < hi; b += 8) {
-      float4 v[8];
-      float vb[8];
+    for (int b = lo; b < hi; b += kAhead) {
+      float4 v[kAhead][kJoinVec];
+      float vb[kAhead];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const size_t slot = (size_t)(b + u) * 2 + (b + u == b0 ? 1 : 0);
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        vb[u] = 0.0f;
-        if (b + u < hi && c < H) v[u] = *reinterpret_cast<const float4*>(part + slot * H + c);
-        if (b + u < hi && blockIdx.y == 0) vb[u] = part_b[slot];
+#pragma unroll
+        for (int i = 0; i < kJoinVec; ++i) {
+          v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b + u < hi && column(i) < H) v[u][i] = *reinterpret_cast<const float4*>(part + slot * H + column(i));
+        }
+        vb[u] = b + u < hi && blockIdx.y == 0 ? part_b[slot] : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        acc.x += v[u].x, acc.y += v[u].y, acc.z += v[u].z, acc.w += v[u].w;
+      for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+        for (int i = 0; i < kJoinVec; ++i)
+          acc[i].x += v[u][i].x, acc[i].y += v[u][i].y, acc[i].z += v[u][i].z, acc[i].w += v[u][i].w;
         bias += vb[u];
       }
     }
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < kJoinVec; ++i) s_acc[group - 1][i][l] = acc[i];
+      if (l == 0) s_bias[group - 1] = bias;
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 0; g < 3; ++g) {
+#pragma unroll
+        for (int i = 0; i < kJoinVec; ++i) {
+          const float4 v = s_acc[g][i][l];
+          acc[i].x += v.x, acc[i].y += v.y, acc[i].z += v.z, acc[i].w += v.w;
+        }
+        bias += s_bias[g];
+      }
+    }
   }
-  if (group > 0) {
-    s_acc[group - 1][l] = acc;
-    if (l == 0) s_bias[group - 1] = bias;
-  }
-  __syncthreads();
   if (group > 0) return;
 #pragma unroll
-  for (int g = 0; g < 3; ++g) {
-    const float4 v = s_acc[g][l];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-    bias += s_bias[g];
-  }
-  if (c < H) *reinterpret_cast<float4*>(dwr + (size_t)e * H + c) = acc;
+  for (int i = 0; i < kJoinVec; ++i)
+    if (column(i) < H) *reinterpret_cast<float4*>(dwr + (size_t)e * H + column(i)) = acc[i];
   if (dbias && blockIdx.y == 0 && threadIdx.x == 0) dbias[e] = bias;
 }
 
-// Pairs per piece: two pieces per SM (32.3 us at 32768 pairs of 384 experts; three: 34.6, four: 35.5: more parts to
+// Pairs per piece: two pieces per SM (at 32768 pairs of 384 experts three cost 2 us more, four 3 us: more parts to
 // add), 8 at least (a CTA's serial walk is the time then) and 128 at most.
 int route_bwd_chunk(int P) {
   const int c = (P + 2 * 148 - 1) / (2 * 148);
@@ -263,8 +280,9 @@ cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w,
                                       status);
     if (err != cudaSuccess) return err;
   }
-  return launch_ex(route_wgrad_join_kernel, dim3((unsigned)E, (unsigned)((H + 255) / 256)), dim3(256), 0, s,
-                   pdl && P > 0, offsets, P, E, H, chunk, (const float*)part, (const float*)part_b, dwr, dbias,
+  constexpr int kJoinCols = 256 * kJoinVec;
+  return launch_ex(route_wgrad_join_kernel, dim3((unsigned)E, (unsigned)((H + kJoinCols - 1) / kJoinCols)), dim3(256),
+                   0, s, pdl && P > 0, offsets, P, E, H, chunk, (const float*)part, (const float*)part_b, dwr, dbias,
                    status);
 }
 

@@ -563,6 +563,58 @@ def test_other_streams_and_replayed_graphs(layers):
     assert L.status() == 0
 
 
+def test_rows_past_32_bit_offsets(layers):
+    """More than 2^31 elements in the sorted rows: the last rows are where they belong."""
+    T, K, E, H = 65536, 9, 16, 4096  # 2.4e9 elements
+    L, P = layers(H, E, K), T * K
+    inv = torch.arange(P, device="cuda", dtype=torch.int32).flip(0).view(T, K).contiguous()
+    x, w = _rand(1, T, H), torch.rand(T, K, device="cuda")
+    xs = L.dispatch(x, inv)
+    tok = torch.tensor([0, 1, T // 2, T - 1], device="cuda")
+    for k in (0, K - 1):
+        assert torch.equal(xs[inv[tok, k].long()], x[tok])
+    ref, mag = R.dispatch_bwd(xs, inv[tok])
+    _within(L.dispatch_bwd(xs, inv)[tok], ref, K * U * mag + R.BF16_HALF * ref.abs() * 1.01, "dx")
+    ref, mag = R.combine(xs, w[tok], inv[tok])
+    _within(L.combine_weighted(xs, w, inv)[tok], ref, K * U * mag + R.BF16_HALF * ref.abs() * 1.01, "out")
+    dy, dw = L.combine_weighted_bwd(x, xs, w, inv)
+    want, ref, mag = R.combine_bwd(x[tok], xs, w[tok], inv[tok])
+    _within(dy[inv[tok].long()], want, want.abs() * (R.BF16_HALF + 2 * U), "dy")
+    _within(dw[tok], ref, (H + 1) * U * mag * 1.01, "dw")
+    assert L.status() == 0
+
+
+def test_activation_and_products_past_32_bit_offsets(layers):
+    """The same for the activation's rows, the products' rows and the weights' gradient (more than 2^31 elements)."""
+    rows, I = 540672, 2048
+    L = layers(256, 8, 1, I)
+    gu = torch.zeros((rows, 2 * I), dtype=BF16, device="cuda")
+    gu[-3:] = _rand(2, 3, 2 * I)
+    h, q, s = L.swiglu_ckpt(gu)
+    small = L.swiglu_ckpt(gu[-3:])
+    assert all(torch.equal(a[-3:], b) for a, b in zip((h, q, s), small))
+    dh = _rand(3, 3, I)
+    h[-3:] = dh
+    dgu = L.swiglu_ckpt_bwd(q, s, h)[0]
+    assert torch.equal(dgu[-3:], L.swiglu_ckpt_bwd(*small[1:], dh)[0])
+    off = torch.zeros(9, dtype=torch.int32, device="cuda")
+    off[8], off[7] = rows, rows - 3
+    wt = _rand(4, 8, 128, 2 * I)
+    got = L.expert_product(gu, wt, off)
+    assert torch.equal(got[-3:], L.expert_product(gu[-3:], wt, (off - (rows - 3)).clamp(min=0)))
+    back = L.expert_product(got, wt, off, transposed=True)
+    assert torch.equal(back[-3:], L.expert_product(got[-3:], wt, (off - (rows - 3)).clamp(min=0), transposed=True))
+    del gu, h, q, s, dgu, got, back
+    E, n = 530, 2048  # 2.2e9 elements of dw
+    L = layers(256, E, 1, 128)
+    off = torch.arange(E + 1, device="cuda", dtype=torch.int32)
+    a, dy = _ints(5, E, n), _ints(6, E, n)
+    dw = L.expert_wgrad(dy, a, off)
+    for e in (0, E - 1):
+        assert torch.equal(dw[e], dy[e][:, None] * a[e][None, :])
+    assert L.status() == 0
+
+
 STEP = [(1, 256, 8, 2, 128), (37, 256, 8, 2, 256), (300, 512, 48, 4, 256)]
 
 

@@ -42,7 +42,7 @@ def routing(T, K, E, seed, drop=0.0, drop_token=None, skew=1.1):
 def gathered(rows, inv):
     """rows[inv] with zeros for dropped pairs, whatever the rows behind them hold: [T, K, H]."""
     kept = (inv >= 0)[..., None]
-    return torch.where(kept, rows.to(F64)[inv.clamp(min=0).long()], torch.zeros((), dtype=F64, device=rows.device))
+    return torch.where(kept, rows[inv.clamp(min=0).long()].to(F64), torch.zeros((), dtype=F64, device=rows.device))
 
 
 def dispatch_bwd(rows, inv, dl=None, idx=None, wr=None):
