@@ -42,8 +42,8 @@
 //
 // Measured, 48 experts x 683 rows, 4096 x 4096 (1.1 TFLOP): forward and rows'
 // gradient 866 us cold (1270 TFLOP/s) and 900 to 1010 us under the power cap,
-// where cuBLAS' 8192^3 holds 1394; one expert x 8192 rows 192 us (1428; cuBLAS
-// 182). bf16 weights' gradient 930 to 1100 us, fp32 1060 to 1250 us (3.2 GB
+// where cuBLAS' 8192^3 holds 1394; one expert x 32768 rows 879 us there (1251;
+// cuBLAS 1345). bf16 weights' gradient 930 to 1100 us, fp32 1060 to 1250 us (3.2 GB
 // written). 333 rows: 251 us for the 1.6 GB of weights (98% of a copy's rate).
 // What made the difference: expect_tx and waits without cluster-scope release
 // and acquire (1693 -> 916 us); whole sectors and TMA stores in the epilogue
@@ -64,6 +64,10 @@ namespace {
 constexpr int kTileM = 256;  // features per CTA pair
 constexpr int kTileN = 256;
 constexpr int kStages = 6;
+// N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost, one
+// expert of 32768 rows re-read its rows from HBM for every M tile (1166 us under the power cap; 879 us in bands of 8, 864
+// in bands of 4; the weights' gradient is 1% faster in bands of 8).
+constexpr int kBand = 8;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
@@ -289,13 +293,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // kWG: the raw rows of a tile's expert are read one tile ahead, so that no role waits for them between tiles.
   const int per_expert = m_tiles * n_tiles_w;
   auto ahead = [&](int tile) { return kWG && tile < total ? expert_rows(a.offsets, tile / per_expert) : Rows{0, 0}; };
+  // Tile r of an expert with nti N tiles: bands of kBand N tiles, M tiles within a band, the band's N tiles innermost,
+  // so that the tiles in flight (one per CTA pair) share their operands in both directions.
+  auto raster = [&](int r, int nti, int& mt, int& nt) {
+    const int band = r / (kBand * m_tiles);
+    const int width = min(kBand, nti - band * kBand);
+    const int q = r - band * kBand * m_tiles;
+    mt = q / width;
+    nt = band * kBand + q - mt * width;
+  };
   auto decode = [&](int tile, const Rows& raw) {
     Tile t;
     if (kWG) {
       t.e = tile / per_expert;
-      const int r = tile - t.e * per_expert;
-      t.m0 = (r / n_tiles_w) * kTileM;
-      t.n0 = (r % n_tiles_w) * kTileN;
+      int mt, nt;
+      raster(tile - t.e * per_expert, n_tiles_w, mt, nt);
+      t.m0 = mt * kTileM;
+      t.n0 = nt * kTileN;
       t.n = min(kTileN, a.n_total - t.n0);
       const Rows rows = raw.within(a.P, a.status);
       t.row0 = rows.begin;
@@ -307,11 +321,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (prefix[mid] * m_tiles <= tile) lo = mid;
         else hi = mid;
       }
-      const int nti = prefix[lo + 1] - prefix[lo];
-      const int r = tile - prefix[lo] * m_tiles;
-      const int nt = r % nti;
+      int mt, nt;
+      raster(tile - prefix[lo] * m_tiles, prefix[lo + 1] - prefix[lo], mt, nt);
       t.e = lo;
-      t.m0 = (r / nti) * kTileM;
+      t.m0 = mt * kTileM;
       t.row0 = first_row[lo] + nt * kTileN;
       t.rows = min(kTileN, n_rows[lo] - nt * kTileN);
       t.n0 = 0;
