@@ -544,10 +544,10 @@ class MoeLayer:
             return None  # the call will fail its own checks; there is no CPU path
         return torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def _out(self, t, name, dtype, shape):
-        """The caller's output tensor, checked, or a new one."""
+    def _out(self, t, name, dtype, shape, like):
+        """The caller's output tensor, checked, or a new one beside the (checked) tensor `like`."""
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
         _want(t, name, dtype, shape, self.device)
         return t
 
@@ -565,7 +565,7 @@ class MoeLayer:
             _want(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
         _want(x, "x", x.dtype if x_scales is None else torch.uint8, (T, self.H), self.device)
         _want(inv, "inv", torch.int32, (T, self.K), self.device)
-        out = self._out(out, "out", dtype, (T * self.K, self.H))
+        out = self._out(out, "out", dtype, (T * self.K, self.H), x)
         moe_dispatch(self.ctx, x, x_scales, kind, inv, T, out, self._stream())
         return out
 
@@ -583,7 +583,7 @@ class MoeLayer:
             _want(dlogit, "dlogit", torch.float32, (T, self.K), self.device)
             _want(topk_idx, "topk_idx", torch.int32, (T, self.K), self.device)
             _want(w_router, "w_router", torch.float32, (self.E, self.H), self.device)
-        out = self._out(out, "out", dx_sorted.dtype, (T, self.H))
+        out = self._out(out, "out", dx_sorted.dtype, (T, self.H), dx_sorted)
         moe_dispatch_bwd(self.ctx, dx_sorted, kind, inv, dlogit, topk_idx, w_router, T, out, self._stream())
         return out
 
@@ -598,7 +598,7 @@ class MoeLayer:
         _want(inv, "inv", torch.int32, (T, self.K), self.device)
         _want(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
         _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
-        out = self._out(out, "out", y_sorted.dtype, (T, self.H))
+        out = self._out(out, "out", y_sorted.dtype, (T, self.H), y_sorted)
         moe_combine_weighted(self.ctx, y_sorted, kind, topk_w, inv, T, out, self._stream())
         return out
 
@@ -614,8 +614,8 @@ class MoeLayer:
         _want(y_sorted, "y_sorted", y_sorted.dtype, (T * self.K, self.H), self.device)
         _want(dout, "dout", y_sorted.dtype, (T, self.H), self.device)
         _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
-        out = self._out(out, "out", y_sorted.dtype, (T * self.K, self.H))
-        dw = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
+        out = self._out(out, "out", y_sorted.dtype, (T * self.K, self.H), y_sorted)
+        dw = torch.empty_like(topk_w)
         moe_combine_weighted_bwd(self.ctx, dout, y_sorted, kind, topk_w, inv, T, out, dw, self._stream())
         return out, dw
 
@@ -637,9 +637,9 @@ class MoeLayer:
         rows, I = self._pair_rows(gu, "gu", inv), self.I
         _want(gu, "gu", torch.bfloat16, (rows, 2 * I), self.device)
         h, q, s = out if out is not None else (None, None, None)
-        h = self._out(h, "h", torch.bfloat16, (rows, I))
-        q = self._out(q, "q", torch.uint8, (rows, 2 * I))
-        s = self._out(s, "s", torch.float32, (rows, 2 * I // 128))
+        h = self._out(h, "h", torch.bfloat16, (rows, I), gu)
+        q = self._out(q, "q", torch.uint8, (rows, 2 * I), gu)
+        s = self._out(s, "s", torch.float32, (rows, 2 * I // 128), gu)
         moe_swiglu_ckpt(self.ctx, gu, inv, rows, h, q, s, self._stream())
         return h, q, s
 
@@ -660,10 +660,10 @@ class MoeLayer:
                 raise ValueError(f"dh: {rows} rows are not a whole number of tokens of {self.K} pairs")
         dgu, hw = out if out is not None else (None, None)
         dw = None
-        dgu = self._out(dgu, "dgu", torch.bfloat16, (rows, 2 * I))
+        dgu = self._out(dgu, "dgu", torch.bfloat16, (rows, 2 * I), dh)
         if topk_w is not None:
-            hw = self._out(hw, "hw", torch.bfloat16, (rows, I))
-            dw = torch.empty((rows // self.K, self.K), dtype=torch.float32, device=self.device)
+            hw = self._out(hw, "hw", torch.bfloat16, (rows, I), dh)
+            dw = torch.empty_like(topk_w)
         elif hw is not None:
             raise ValueError("hw: only with topk_w")
         moe_swiglu_ckpt_bwd(self.ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dw, self._stream())
@@ -686,10 +686,10 @@ class MoeLayer:
         _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
         _want(perm_src, "perm_src", torch.int32, (P,), self.device)
         _want(perm_k, "perm_k", torch.int32, (P,), self.device)
-        ws = torch.empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8, device=self.device)
-        dl = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
-        dwr = torch.empty((self.E, self.H), dtype=torch.float32, device=self.device)
-        db = torch.empty((self.E,), dtype=torch.float32, device=self.device)
+        ws = x.new_empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8)
+        dl = torch.empty_like(topk_w)
+        dwr = topk_w.new_empty((self.E, self.H))
+        db = topk_w.new_empty(self.E)
         moe_route_bwd(self.ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dl, dwr, db, ws,
                       self._stream())
         return dl, dwr, db
@@ -712,7 +712,7 @@ class MoeLayer:
         _want(w, "w", torch.bfloat16, (self.E, n_out, n_in), self.device)
         _want(a, "a", torch.bfloat16, (P, k), self.device)
         _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
-        out = self._out(out, "out", torch.bfloat16, (P, m))
+        out = self._out(out, "out", torch.bfloat16, (P, m), a)
         moe_expert_product(self.ctx, a, w, offsets, P, n_in, n_out, transposed, out, self._stream())
         return out
 
@@ -733,7 +733,7 @@ class MoeLayer:
             raise ValueError("accumulate: needs the tensor to add to (out)")
         if dtype not in _ROW_TYPES:
             raise TypeError("dtype: expected bf16 or fp32")
-        out = self._out(out, "out", dtype, (self.E, n_out, n_in))
+        out = self._out(out, "out", dtype, (self.E, n_out, n_in), dy)
         moe_expert_wgrad(self.ctx, dy, a, offsets, P, n_in, n_out, _ROW_TYPES[dtype], accumulate, out, self._stream())
         return out
 
