@@ -29,11 +29,14 @@
 // A bf16 gradient is one run (its rounding, 2^-9, is larger up to a million
 // rows), and so are the other two forms (K at most 16384).
 //
-// In the weights' gradient K is the expert's own rows: the last K step of an
-// expert may hold rows of the next one (or of no expert at all, with any
-// bits in them). Those rows are zeroed in shared memory, in both operands,
-// before the MMA of that step sees them, by a warp of its own; K-16 steps
-// with no row of the expert are not issued.
+// In the weights' gradient K is the expert's own rows. Whole groups of 16 rows
+// (one MMA's K) go through the stages; groups that reach into the next expert's
+// rows are not issued. The last 1 to 15 rows of an expert come as a box of 16
+// rows of their own, whose other rows (the next expert's, or anything behind
+// the last one) a warp of each CTA zeroes in both operands before the MMA may
+// read them. The box is fetched when the tile's first stage is, so that neither
+// the zeros nor their publication to the other CTA (a release at cluster scope,
+// 4-5% of an fp32 gradient when it sat in the last stage) is waited for.
 //
 // Warp roles: 0..3 epilogue (TMEM -> registers -> global), 4 TMA producer,
 // 5 TMEM allocation and, in the leader CTA, the MMA issuer, 6 the tail's
@@ -63,7 +66,8 @@ namespace {
 
 constexpr int kTileM = 256;  // features per CTA pair
 constexpr int kTileN = 256;
-constexpr int kStages = 6;
+// K steps in flight: the weights' gradient gives one up for its tails and a third store box per warp.
+__host__ __device__ constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
 // N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost, one
 // expert of 32768 rows re-read its rows from HBM for every M tile (1166 us under the power cap; 879 us in bands of 8, 864
 // in bands of 4; the weights' gradient is 1% faster in bands of 8).
@@ -71,6 +75,7 @@ constexpr int kBand = 8;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
+__host__ __device__ constexpr int barriers(bool wgrad) { return 2 * stages(wgrad) + 10; }
 // K steps summed in TMEM before an fp32 gradient goes out. The tensor cores' running sum loses about 1.4e-9 of itself
 // per row: a gradient over 16384 rows summed in one run was 1.9e-5 off (2-norm), over 65536 rows 7.6e-5. In segments of
 // 14 steps (896 rows) it stays under 1e-6 for any number of rows. Time at 8192 rows, 4096 x 4096: 238 us in one run,
@@ -78,11 +83,14 @@ constexpr int kThreads = 224;
 constexpr int kSegment = 14;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
 constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes
-// Output staging: two store boxes per epilogue warp (weights' gradient), or
-// two pieces of 32 rows x 128 features (the other forms).
-constexpr uint32_t kStagingBytes = 8 * kStoreBox;
-constexpr uint32_t kPieceBytes = 32 * 256;
-__host__ __device__ constexpr uint32_t staging_bytes(bool wgrad) { return wgrad ? kStagingBytes : 2 * kPieceBytes; }
+constexpr uint32_t kPieceBytes = 32 * 256;        // 32 rows x 128 features
+// Output staging: kBoxes store boxes per epilogue warp (weights' gradient), or two pieces.
+constexpr int kBoxes = 3;
+__host__ __device__ constexpr uint32_t staging_bytes(bool wgrad) {
+  return wgrad ? 4 * kBoxes * kStoreBox : 2 * kPieceBytes;
+}
+constexpr uint32_t kTailBox = 16 * 128;           // weights' gradient: 16 rows x 64 elements
+constexpr uint32_t kTailBytes = 4 * kTailBox;     // two boxes of the M operand, two of the N operand
 
 enum Form { kForward = 0, kRowGrad = 1, kWeightGrad = 2 };
 
@@ -110,6 +118,28 @@ __device__ __forceinline__ void cluster_sync() {
 
 __device__ __forceinline__ void remote_arrive(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// With the writes of this thread's CTA before it, for an MMA that reads them from the other one.
+__device__ __forceinline__ void remote_publish(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Bounded wait for what remote_publish released.
+__device__ __forceinline__ bool wait_published(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
 }
 
 // Relaxed: it publishes no data of this thread (the copies' bytes order themselves).
@@ -169,11 +199,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-// MN-major operand in 128-byte swizzled boxes of 64 K rows x 64 elements:
-// groups of 8 K rows 1024 bytes apart (stride byte offset), the next 64
-// elements one box further (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
+// MN-major operand in 128-byte swizzled boxes of K rows x 64 elements: groups
+// of 8 K rows 1024 bytes apart (stride byte offset), the next 64 elements one
+// box further (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t box_bytes) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(box_bytes >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
 }
@@ -223,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr bool kWG = FORM == kWeightGrad;
   constexpr bool kMmn = FORM != kForward;  // the M operand is MN-major
   constexpr bool kNmn = kWG;               // so is the N operand
+  constexpr int kStages = stages(kWG);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
@@ -232,14 +263,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t staging = base + kStages * kStageBytes;  // 1024-byte aligned
-  const uint32_t bars = staging + staging_bytes(kWG);
+  const uint32_t staging = base + kStages * kStageBytes;  // 1024-byte aligned, as are the tails
+  const uint32_t tails = staging + staging_bytes(kWG);
+  const uint32_t bars = tails + (kWG ? 2 * kTailBytes : 0);
   auto full = [&](int s) { return bars + 8u * s; };  // in the leader CTA; one arrival per CTA and the bytes of both
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-  auto landed = [&](int s) { return bars + 8u * (2 * kStages + s); };  // tail steps, before the zeros
-  auto tfull = [&](int b) { return bars + 8u * (3 * kStages + b); };
-  auto tempty = [&](int b) { return bars + 8u * (3 * kStages + 2 + b); };  // in the leader CTA
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * kStages + 4));
+  auto tfull = [&](int b) { return bars + 8u * (2 * kStages + b); };
+  auto tempty = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };  // in the leader CTA
+  // tail boxes: landed (before the zeros), ready (in the leader CTA; one arrival per CTA), free
+  auto tail_landed = [&](int b) { return bars + 8u * (2 * kStages + 4 + b); };
+  auto tail_ready = [&](int b) { return bars + 8u * (2 * kStages + 6 + b); };
+  auto tail_free = [&](int b) { return bars + 8u * (2 * kStages + 8 + b); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * barriers(kWG));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* ep_abort = reinterpret_cast<volatile int*>(tmem_slot + 2);  // written by epilogue warps only
   // not in kWG: [E + 1] N tiles before each expert, [E] its first row, [E] its rows
@@ -250,11 +285,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 2);
       mbar_init(empty(s), 1);
-      mbar_init(landed(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), 8);  // four epilogue warps of each CTA
+      mbar_init(tail_landed(b), 1);
+      mbar_init(tail_ready(b), 2);
+      mbar_init(tail_free(b), 1);
     }
     *abort_flag = 0;
     *ep_abort = 0;
@@ -335,12 +372,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // An fp32 gradient over many rows is summed in segments of at most kSegment K steps: the first is stored, the others
   // are added in L2.
   auto segments = [&](int KB) { return kWG && a.out_f32 && KB > kSegment ? (KB + kSegment - 1) / kSegment : 1; };
-  auto k_steps = [&](const Tile& t) { return kWG ? (t.rows + 63) / 64 : a.k_total / 64; };
+  auto k_steps = [&](const Tile& t) { return kWG ? (t.rows + 48) / 64 : a.k_total / 64; };  // steps with a whole group
+  auto tail_rows = [&](const Tile& t) { return kWG ? t.rows & 15 : 0; };
 
   if (warp == 4) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
-      int issued = 0;
+      int issued = 0, n_tails = 0;
       Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total && !*abort_flag; tile += n_clusters) {
         const Tile t = decode(tile, raw);
@@ -348,6 +386,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int KB = k_steps(t);
         const int half = t.n / 2;  // this CTA's part of the N operand
         const int mrow = t.m0 + (int)rank * 128;
+        if (tail_rows(t)) {
+          const int b = n_tails & 1;
+          if (n_tails >= 2 && !mbar_wait(tail_free(b), ((n_tails >> 1) - 1) & 1)) {
+            *abort_flag = 1;
+            flag_status(a.status, MOE_DEV_TIMEOUT);
+            break;
+          }
+          ++n_tails;
+          const uint32_t at = tails + b * kTailBytes, bar = map_rank(tail_landed(b), rank);
+          const int row = t.row0 + (t.rows & ~15);
+          mbar_arrive_expect_tx(tail_landed(b), (2 + half / 64) * kTailBox);
+          tma_load_pair(at, &maps.n[2], bar, mrow, row);
+          tma_load_pair(at + kTailBox, &maps.n[2], bar, mrow + 64, row);
+          for (int j = 0; j < half / 64; ++j)
+            tma_load_pair(at + (2 + j) * kTailBox, &maps.n[1], bar, t.n0 + (int)rank * half + 64 * j, row);
+        }
         // K-major N operand: one box of 16, 32, 64 or 128 rows
         const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
         const uint32_t bytes = kOpBytes + (kNmn ? (uint32_t)(half / 64) * kBoxBytes : (16u << bi) * 128u);
@@ -359,15 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
-          const bool tail = kWG && kb == KB - 1 && (t.rows & 63);
-          uint32_t bar;
-          if (tail) {
-            bar = map_rank(landed(s), rank);
-            mbar_arrive_expect_tx(landed(s), bytes);
-          } else {
-            bar = map_rank(full(s), 0);
-            remote_expect_tx(bar, bytes);
-          }
+          const uint32_t bar = map_rank(full(s), 0);
+          remote_expect_tx(bar, bytes);
           if (FORM == kForward) {
             tma_load_pair(sa, &maps.m, bar, kb * 64, t.e * a.m_total + mrow);
           } else {
@@ -388,18 +435,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0)
         for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
           mbar_wait(full(g % kStages), (g / kStages) & 1);
+      for (int g = n_tails - 2 < 0 ? 0 : n_tails - 2; g < n_tails; ++g) mbar_wait(tail_landed(g & 1), (g >> 1) & 1);
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0 && lane == 0) {
-      int consumed = 0, j = 0;
+      int consumed = 0, j = 0, n_tails = 0;
       Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total; tile += n_clusters) {
         const Tile t = decode(tile, raw);
         raw = ahead(tile + n_clusters);
-        const int KB = k_steps(t);
-        if (KB == 0) continue;  // an expert without rows: the epilogue writes zeros
-        const int nseg = segments(KB);
+        if (t.rows == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const int KB = k_steps(t), nseg = segments(KB);
         const uint32_t idesc =
             instr_desc(256, t.n, 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
         bool ok = true;
@@ -409,6 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem + buf * kTileN;
           const int kb0 = (int)((long long)KB * seg / nseg), kb1 = (int)((long long)KB * (seg + 1) / nseg);
+          uint32_t accumulate = 0;
           for (int kb = kb0; ok && kb < kb1; ++kb, ++consumed) {
             const int s = consumed % kStages;
             if (!mbar_wait(full(s), (consumed / kStages) & 1)) {
@@ -417,15 +465,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
-            const int left = t.rows - kb * 64;
-            const int ks = kWG ? (left >= 64 ? 4 : (left + 15) / 16) : 4;
+            const int ks = kWG ? min(4, (t.rows - kb * 64) >> 4) : 4;  // whole groups of this step
 #pragma unroll 4
             for (int k = 0; k < ks; ++k) {
-              const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048) : sw128_kmajor_desc(sa + k * 32);
-              const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048) : sw128_kmajor_desc(sb + k * 32);
-              mma_pair(d, ad, bd, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
+              const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048, kBoxBytes) : sw128_kmajor_desc(sa + k * 32);
+              const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048, kBoxBytes) : sw128_kmajor_desc(sb + k * 32);
+              mma_pair(d, ad, bd, idesc, accumulate);
+              accumulate = 1;
             }
             commit_pair(empty(s));
+          }
+          if (ok && seg == nseg - 1 && tail_rows(t)) {
+            const int b = n_tails & 1;
+            ok = wait_published(tail_ready(b), (n_tails >> 1) & 1);
+            ++n_tails;
+            if (ok) {
+              tc_fence_after();
+              const uint32_t at = tails + b * kTailBytes;
+              mma_pair(d, sw128_mnmajor_desc(at, kTailBox), sw128_mnmajor_desc(at + 2 * kTailBox, kTailBox), idesc,
+                       accumulate);
+              commit_pair(tail_free(b));
+            }
           }
           commit_pair(tfull(buf));
         }
@@ -437,22 +497,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 6) {
-    // --------------------------------------------- zeros of the tail K steps
+    // ---------------------------------------------------- zeros of the tails
     if (kWG) {
-      int before = 0;
-      uint32_t phases = 0;  // bit s: parity of the next use of landed(s)
+      int n_tails = 0;
       Rows raw = ahead(cluster);
       for (int tile = cluster; tile < total; tile += n_clusters) {
         const Tile t = decode(tile, raw);
         raw = ahead(tile + n_clusters);
-        const int KB = k_steps(t);
-        before += KB;
-        const int rem = t.rows & 63;
+        const int rem = tail_rows(t);
         if (rem == 0) continue;
-        const int s = (before - 1) % kStages;
+        const int b = n_tails & 1;
         // every lane waits itself: each writes over bytes that the copy brought
-        const int ok = __all_sync(0xffffffffu, mbar_wait(landed(s), (phases >> s) & 1));
-        phases ^= 1u << s;
+        const int ok = __all_sync(0xffffffffu, mbar_wait(tail_landed(b), (n_tails >> 1) & 1));
+        ++n_tails;
         if (!ok) {
           if (lane == 0) {
             *abort_flag = 1;
@@ -460,16 +517,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           break;
         }
-        const int upto = (rem + 15) & ~15;
         const int boxes = 2 + t.n / 128;  // M operand, then this CTA's part of the N operand
-        const int vecs = (upto - rem) * 8;
-        for (int b = 0; b < boxes; ++b) {
-          uint8_t* box = gbase + s * kStageBytes + b * kBoxBytes + rem * 128;
-          for (int v = lane; v < vecs; v += 32) *reinterpret_cast<uint4*>(box + v * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
+        uint8_t* at = gbase + (tails - base) + b * kTailBytes + rem * 128;
+        for (int x = 0; x < boxes; ++x)
+          for (int v = lane; v < (16 - rem) * 8; v += 32)
+            *reinterpret_cast<uint4*>(at + x * kTailBox + v * 16) = make_uint4(0u, 0u, 0u, 0u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) remote_arrive(map_rank(full(s), 0));
+        if (lane == 0) remote_publish(map_rank(tail_ready(b), 0));
       }
     }
   } else {
@@ -480,13 +535,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int tile = cluster; tile < total && !gave_up; tile += n_clusters) {
       const Tile t = decode(tile, raw);
       raw = ahead(tile + n_clusters);
-      const int KB = k_steps(t);
-      if (KB == 0 && a.accumulate) continue;  // nothing to add
+      const bool any = t.rows > 0;
+      if (!any && a.accumulate) continue;  // nothing to add
       const bool in_m = t.m0 + (int)rank * 128 < a.m_total;  // CTA-uniform
-      const int nseg = segments(KB);
+      const int nseg = segments(k_steps(t));
       for (int seg = 0; seg < nseg && !gave_up; ++seg) {
         const int buf = j & 1;
-        if (KB > 0) {
+        if (any) {
           if (lane == 0 && !mbar_wait(tfull(buf), (j >> 1) & 1)) *ep_abort = 1;
           named_bar_sync(2, 128);  // the four warps leave the loop together or not at all
           if (*ep_abort) {
@@ -511,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < cols; c += step, ++piece) {
             uint32_t v[32];
             auto load = [&](int at) {
-              if (KB > 0) {
+              if (any) {
                 tmem_ld32(tl + at, v);
                 tmem_wait_ld();
               } else {
@@ -521,9 +576,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             if (kWG) {
               // this lane's 128-byte row of the box, 16-byte chunks swizzled as the store expects them
-              const uint32_t at = staging + (warp * 2 + (piece & 1)) * kStoreBox;
+              const uint32_t at = staging + (warp * kBoxes + piece % kBoxes) * kStoreBox;
               uint8_t* row = gbase + (at - base) + lane * 128;
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box is free again
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");  // the box is free again
               __syncwarp();
               if (a.out_f32) {
                 load(c);
@@ -572,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (KB > 0) {
+        if (any) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
@@ -597,8 +652,8 @@ template <int FORM>
 cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long max_tiles, int num_sms,
                         cudaStream_t s) {
   constexpr bool kWG = FORM == kWeightGrad;
-  const size_t smem = 1024 + (size_t)kStages * kStageBytes + staging_bytes(kWG) + 8 * (3 * kStages + 4) + 16 +
-                      (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
+  const size_t smem = 1024 + (size_t)stages(kWG) * kStageBytes + staging_bytes(kWG) + (kWG ? 2 * kTailBytes : 0) +
+                      8 * barriers(kWG) + 16 + (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
   const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

@@ -27,7 +27,10 @@ cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w,
                              float* dwr, float* dbias, float* ws, int* status, cudaStream_t s, bool pdl);
 
 // Tensor maps of one expert product: the M operand (weights, or dy), the N
-// operand (rows) and the output of the weights' gradient; the K-major N operand has one map per box height 16 << i.
+// operand (rows) and the output of the weights' gradient. A K-major N operand
+// has one map per box height 16 << i; in the weights' gradient n[0] is the N
+// operand in boxes of 64 rows, n[1] and n[2] the N and the M operand in boxes
+// of 16.
 struct alignas(64) ProductMaps {
   CUtensorMap m;
   CUtensorMap n[4];

@@ -276,7 +276,9 @@ moe_status_t moe_expert_wgrad(moe_ctx_t* ctx, const void* dy, const void* a, con
   ProductMaps maps;
   if ((st = encode(ctx, &maps.m, dy, n_out, P, 64)) != MOE_OK) return st;
   if ((st = encode(ctx, &maps.n[0], a, n_in, P, 64)) != MOE_OK) return st;
-  for (int i = 1; i < 4; ++i) maps.n[i] = maps.n[0];
+  if ((st = encode(ctx, &maps.n[1], a, n_in, P, 16)) != MOE_OK) return st;
+  if ((st = encode(ctx, &maps.n[2], dy, n_out, P, 16)) != MOE_OK) return st;
+  maps.n[3] = maps.n[2];  // not used in this form
   if ((st = encode(ctx, &maps.out, dw, n_in, (uint64_t)E * n_out, 32, dtype == MOE_T_F32)) != MOE_OK) return st;
   ProductArgs args{offsets, E, P, n_out, n_in, 0, dw, dtype == MOE_T_F32, accumulate, ctx->d_status};
   Prof p(ctx, MOE_PROF_PRODUCT, s);
