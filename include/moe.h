@@ -405,9 +405,9 @@ size_t moe_route_bwd_workspace_size(const moe_ctx_t* ctx, int T);
  *   written whole (zeros for experts without pairs). ws: 256-byte aligned;
  *   calls that may overlap need workspaces of their own. */
 moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales, const float* topk_w,
-                           const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T,
-                           float* dlogit, float* dw_router, float* dlogit_bias, void* ws, size_t ws_bytes,
-                           moe_stream_t stream);
+                           const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src,
+                           const int32_t* perm_k, int T, float* dlogit, float* dw_router, float* dlogit_bias, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
 
 /* One product per expert over its sorted rows p = offsets[e] .. offsets[e+1]-1
  * (tensor cores, fp32 accumulation, one rounding), w [E, n_out, n_in] bf16:

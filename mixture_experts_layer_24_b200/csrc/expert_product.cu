@@ -11,8 +11,8 @@
 //
 // Two CTAs of a cluster (one TPC) compute one 256 x 256 tile with
 // cta_group::2: each stages 128 rows of the M operand and half of the N
-// operand (32 KB per 64-deep K step), so a pair moves half the bytes from L2
-// that two separate 128 x 256 tiles would. M is the feature axis, so its tiles
+// operand (32 KB per 64-deep K step), two thirds of the bytes that two separate
+// 128 x 256 tiles would bring from L2. M is the feature axis, so its tiles
 // are always full; N is the expert's rows in the first two forms (the MMA
 // width follows the rows left, in steps of 32), the input features in the
 // third.
@@ -46,8 +46,8 @@
 // Measured, 48 experts x 683 rows, 4096 x 4096 (1.1 TFLOP): forward and rows'
 // gradient 866 us cold (1270 TFLOP/s) and 900 to 1010 us under the power cap,
 // where cuBLAS' 8192^3 holds 1394; one expert x 32768 rows 879 us there (1251;
-// cuBLAS 1345). bf16 weights' gradient 930 to 1100 us, fp32 1060 to 1250 us (3.2 GB
-// written). 333 rows: 251 us for the 1.6 GB of weights (98% of a copy's rate).
+// cuBLAS 1345). bf16 weights' gradient 930 us cold and 1150 capped, fp32 1060
+// and 1300 us (3.2 GB written). 333 rows: 251 us for the 1.6 GB of weights (98% of a copy's rate).
 // What made the difference: expect_tx and waits without cluster-scope release
 // and acquire (1693 -> 916 us); whole sectors and TMA stores in the epilogue
 // (fp32 gradient 2154 -> 1207 us). What did not: bringing weights into L2
@@ -68,9 +68,9 @@ constexpr int kTileM = 256;  // features per CTA pair
 constexpr int kTileN = 256;
 // K steps in flight: the weights' gradient gives one up for its tails and a third store box per warp.
 __host__ __device__ constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
-// N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost, one
-// expert of 32768 rows re-read its rows from HBM for every M tile (1166 us under the power cap; 879 us in bands of 8, 864
-// in bands of 4; the weights' gradient is 1% faster in bands of 8).
+// N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost,
+// one expert of 32768 rows re-read its rows from HBM for every M tile (1166 us under the power cap; 879 us in bands of
+// 8, 864 in bands of 4; the weights' gradient is 1% faster in bands of 8).
 constexpr int kBand = 8;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
@@ -468,8 +468,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int ks = kWG ? min(4, (t.rows - kb * 64) >> 4) : 4;  // whole groups of this step
 #pragma unroll 4
             for (int k = 0; k < ks; ++k) {
-              const uint64_t ad = kMmn ? sw128_mnmajor_desc(sa + k * 2048, kBoxBytes) : sw128_kmajor_desc(sa + k * 32);
-              const uint64_t bd = kNmn ? sw128_mnmajor_desc(sb + k * 2048, kBoxBytes) : sw128_kmajor_desc(sb + k * 32);
+              const uint64_t ad =
+                  kMmn ? sw128_mnmajor_desc(sa + k * 2048, kBoxBytes) : sw128_kmajor_desc(sa + k * 32);
+              const uint64_t bd =
+                  kNmn ? sw128_mnmajor_desc(sb + k * 2048, kBoxBytes) : sw128_kmajor_desc(sb + k * 32);
               mma_pair(d, ad, bd, idesc, accumulate);
               accumulate = 1;
             }
@@ -578,7 +580,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // this lane's 128-byte row of the box, 16-byte chunks swizzled as the store expects them
               const uint32_t at = staging + (warp * kBoxes + piece % kBoxes) * kStoreBox;
               uint8_t* row = gbase + (at - base) + lane * 128;
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");  // the box is free again
+              // the box is free again
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
               __syncwarp();
               if (a.out_f32) {
                 load(c);
@@ -652,8 +655,9 @@ template <int FORM>
 cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long max_tiles, int num_sms,
                         cudaStream_t s) {
   constexpr bool kWG = FORM == kWeightGrad;
+  // 226 KB at most (a CTA may have 227)
   const size_t smem = 1024 + (size_t)stages(kWG) * kStageBytes + staging_bytes(kWG) + (kWG ? 2 * kTailBytes : 0) +
-                      8 * barriers(kWG) + 16 + (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));  // 226 KB at most (a CTA may have 227)
+                      8 * barriers(kWG) + 16 + (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));
   const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

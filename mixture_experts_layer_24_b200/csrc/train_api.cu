@@ -56,7 +56,8 @@ moe_status_t check_rows(const moe_ctx_t* ctx, int rows) {
 }
 
 moe_status_t check_row_type(int dtype) {
-  if (dtype != MOE_T_BF16 && dtype != MOE_T_F32) return fail(MOE_ERR_INVALID_ARG, "dtype must be MOE_T_BF16 or MOE_T_F32");
+  if (dtype != MOE_T_BF16 && dtype != MOE_T_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype must be MOE_T_BF16 or MOE_T_F32");
   return MOE_OK;
 }
 
@@ -74,9 +75,10 @@ moe_status_t encode(const moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uint6
   const cuuint64_t strides[1] = {inner * (f32 ? 4 : 2)};
   const cuuint32_t box[2] = {f32 ? 32u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = ctx->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = ctx->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                 const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
   return MOE_OK;
 }
@@ -211,9 +213,9 @@ size_t moe_route_bwd_workspace_size(const moe_ctx_t* ctx, int T) {
 }
 
 moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales, const float* topk_w,
-                           const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T,
-                           float* dlogit, float* dw_router, float* dlogit_bias, void* ws, size_t ws_bytes,
-                           moe_stream_t stream) {
+                           const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src,
+                           const int32_t* perm_k, int T, float* dlogit, float* dw_router, float* dlogit_bias, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
   moe_status_t st = check_tokens(ctx, T);
   if (st != MOE_OK) return st;
   if (!offsets || !dw_router) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
@@ -229,8 +231,8 @@ moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Prof p(ctx, MOE_PROF_ROUTE_BWD, s);
   ctx->launches.fetch_add(T > 0 ? kRouteBwdLaunches - 1 : 0, std::memory_order_relaxed);  // Prof counts one
-  MOE_CUDA(launch_route_bwd(x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, c.top_k, c.n_experts, c.hidden, dlogit,
-                            dw_router, dlogit_bias, static_cast<float*>(ws), ctx->d_status, s, ctx->chain));
+  MOE_CUDA(launch_route_bwd(x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, c.top_k, c.n_experts, c.hidden,
+                            dlogit, dw_router, dlogit_bias, static_cast<float*>(ws), ctx->d_status, s, ctx->chain));
   return MOE_OK;
 }
 

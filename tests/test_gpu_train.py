@@ -67,7 +67,8 @@ def _within(got, ref, bound, what):
 
 # T, K, E, H, share of dropped pairs, a token that loses all its pairs
 ROWS = [(1, 1, 1, 128, 0.0, None), (1, 8, 384, 4096, 0.0, None), (3, 2, 8, 256, 0.5, 0), (37, 3, 7, 384, 0.1, 36),
-        (257, 8, 48, 512, 0.1, 5), (130, 32, 64, 128, 0.05, 7), (65, 9, 33, 640, 0.0, None), (1001, 4, 48, 1024, 0.3, 0)]
+        (257, 8, 48, 512, 0.1, 5), (130, 32, 64, 128, 0.05, 7), (65, 9, 33, 640, 0.0, None),
+        (1001, 4, 48, 1024, 0.3, 0)]
 
 
 @pytest.mark.parametrize("T,K,E,H,drop,gone", ROWS)
@@ -147,7 +148,8 @@ def test_combine_gradient_against_differences(layers):
 
 
 # rows are T*K pairs of I columns
-ACT = [(1, 1, 128, 0.0), (3, 2, 256, 0.3), (37, 8, 384, 0.1), (129, 3, 2048, 0.0), (5, 4, 8192, 0.2), (700, 8, 128, 0.05)]
+ACT = [(1, 1, 128, 0.0), (3, 2, 256, 0.3), (37, 8, 384, 0.1), (129, 3, 2048, 0.0), (5, 4, 8192, 0.2),
+       (700, 8, 128, 0.05)]
 
 
 def _gate_up(seed, rows, I):
@@ -687,7 +689,8 @@ def test_captured_training_step(layers):
     from mixture_experts_layer_24_b200 import train
     T, H, E, K, I = 33, 256, 8, 2, 256
     L = layers(H, E, K, I)
-    wr, w_gu, w_dn = _rand(72, E, H, std=0.05, dtype=F32), _rand(73, E, 2 * I, H, std=0.06), _rand(74, E, H, I, std=0.06)
+    wr = _rand(72, E, H, std=0.05, dtype=F32)
+    w_gu, w_dn = _rand(73, E, 2 * I, H, std=0.06), _rand(74, E, H, I, std=0.06)
 
     def step(x, dout):
         out, saved = train.forward(L, x, wr, w_gu, w_dn, ckpt_x=True)
