@@ -261,8 +261,8 @@ def moe_route_bwd_workspace_size(ctx, T: int) -> int:
 def moe_route_bwd(ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dlogit, dw_router, dlogit_bias, ws,
                   stream=None):
     _check(lib().moe_route_bwd(ctx, _p(x), _p(x_scales), _p(topk_w), _p(dtopk_w), _p(offsets), _p(perm_src),
-                               _p(perm_k), T, _p(dlogit), _p(dw_router), _p(dlogit_bias), _p(ws), _nbytes(ws), _s(stream)),
-           "moe_route_bwd")
+                               _p(perm_k), T, _p(dlogit), _p(dw_router), _p(dlogit_bias), _p(ws), _nbytes(ws),
+                               _s(stream)), "moe_route_bwd")
 
 
 def moe_expert_product(ctx, a, w, offsets, P, n_in, n_out, transposed, out, stream=None):
@@ -536,7 +536,7 @@ class MoeLayer:
         """Whether a call has to leave the current stream or device first."""
         if stream is not None:
             return True
-        return self.device.type == "cuda" and torch.cuda.current_device() != self.device.index
+        return self.device.type == "cuda" and torch._C._cuda_getDevice() != self.device.index
 
     def _stream(self):
         """The handle of the current stream of this layer's device, which is the current one here."""

@@ -564,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int cols = kWG ? t.n : t.rows;
           // columns per step: a 128-byte store box of the output type, or 32 rows of the output
           const int step = kWG && !a.out_f32 ? 64 : 32;
-  #pragma unroll 1
+#pragma unroll 1
           for (int c = 0; c < cols; c += step, ++piece) {
             uint32_t v[32];
             auto load = [&](int at) {
@@ -572,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld32(tl + at, v);
                 tmem_wait_ld();
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = 0u;
               }
             };
@@ -585,15 +585,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (a.out_f32) {
                 load(c);
-  #pragma unroll
+#pragma unroll
                 for (int q = 0; q < 8; ++q)
                   *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) =
                       make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int half = 0; half < 2; ++half) {
                   load(c + half * 32);
-  #pragma unroll
+#pragma unroll
                   for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<uint4*>(row + (((half * 4 + q) ^ (lane & 7)) << 4)) =
                         make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
@@ -614,13 +614,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // straight from the lanes took three times as long at K = 512).
               uint8_t* buf32 = gbase + (staging - base) + (piece & 1) * kPieceBytes;
               load(c);
-  #pragma unroll
+#pragma unroll
               for (int q = 0; q < 32; ++q)
                 *reinterpret_cast<__nv_bfloat16*>(buf32 + q * 256 + (warp * 32 + lane) * 2) =
                     __float2bfloat16_rn(__uint_as_float(v[q]));
               named_bar_sync(1, 128);  // also: everyone is done reading the piece before last
               __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t.m0 + rank * 128;
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int q = warp * 8 + i * 2 + (lane >> 4), ch = lane & 15;
                 if (c + q < cols)
