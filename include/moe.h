@@ -413,7 +413,8 @@ moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales,
  * (tensor cores, fp32 accumulation, one rounding), w [E, n_out, n_in] bf16:
  *   transposed == 0: out[p, :] = w[e] a[p, :]     a [P, n_in],  out [P, n_out]
  *   transposed != 0: out[p, :] = w[e]^T a[p, :]   a [P, n_out], out [P, n_in]
- * (the forward product and the gradient of its rows). Rows at and behind
+ * (the forward product and the gradient of its rows). A row's bits depend on
+ * that row and its expert's weights alone. Rows at and behind
  * offsets[E] are left as they were. n_in, n_out multiples of 128, at most
  * 16384; 0 <= P <= 65536*32; offsets [E+1] rising from 0 or more to at most P.
  * An expert whose range is not inside [0, P] computes nothing and sets

@@ -1,7 +1,8 @@
 // expert_product.cu -- the per-expert products of a training step on the
 // 5th-generation tensor cores. The rows of expert e are the sorted pairs
 // p = offsets[e] .. offsets[e+1]-1; every output element is one fp32
-// accumulation over its whole K axis, in increasing order, rounded once:
+// accumulation over its whole K axis, in increasing order, rounded once, the
+// same whatever other rows there are (no split of K by the number of tiles):
 //
 //   forward   out[p, o] = sum_i a[p, i] * w[e, o, i]     a [P, n_in],  w [E, n_out, n_in]
 //   rows' gradient

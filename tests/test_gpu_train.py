@@ -339,6 +339,20 @@ def test_expert_product(layers, counts, slack, n_in, n_out, transposed):
         assert (out[n:] == 7).all() and L.status() == 0
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+def test_products_rows_do_not_depend_on_each_other(layers, transposed):
+    """A row's bits are the same alone, among few and among many rows of its expert, at any place in a tile."""
+    E, n_in, n_out = 3, 1024, 640
+    L, k = layers(256, E, 1, 128), n_out if transposed else n_in
+    w, rows = _rand(26, E, n_out, n_in, std=0.1), _rand(27, 700, k)
+    off, _ = _segments([0, 700, 0])
+    many = L.expert_product(rows, w, off, transposed=transposed)
+    for lo, hi in ((0, 1), (5, 38), (255, 257), (400, 699)):
+        few, _ = _segments([0, hi - lo, 0])
+        got = L.expert_product(rows[lo:hi].contiguous(), w, few, transposed=transposed)
+        assert torch.equal(got, many[lo:hi])
+
+
 @pytest.mark.parametrize("counts,slack,n_in,n_out", PROD)
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_expert_wgrad(layers, counts, slack, n_in, n_out, dtype):
