@@ -170,6 +170,20 @@ __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// One lane of a warp that is here together; the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// A value that all lanes hold, for the compiler to know it.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -325,6 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the peer's barriers are initialised before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem_u = (uint32_t)uniform((int)tmem), base_u = (uint32_t)uniform((int)base);
 
   const int n_tiles_w = (a.n_total + kTileN - 1) / kTileN;  // kWG: N tiles of one expert
   const int total = kWG ? a.E * m_tiles * n_tiles_w : prefix[a.E] * m_tiles;
@@ -440,61 +455,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the steps and one lane issues: warp-uniform code keeps descriptors in uniform registers,
+    // without a move to them before each MMA.
+    if (rank == 0) {
       int consumed = 0, j = 0, n_tails = 0;
+      const int n_all = uniform(total);
       Rows raw = ahead(cluster);
-      for (int tile = cluster; tile < total; tile += n_clusters) {
+      for (int tile = cluster; tile < n_all; tile += n_clusters) {
         const Tile t = decode(tile, raw);
         raw = ahead(tile + n_clusters);
-        if (t.rows == 0) continue;  // an expert without rows: the epilogue writes zeros
-        const int KB = k_steps(t), nseg = segments(KB);
+        const int rows = uniform(t.rows);
+        if (rows == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const int KB = uniform(k_steps(t)), nseg = uniform(segments(KB)), tail = uniform(tail_rows(t));
         const uint32_t idesc =
-            instr_desc(256, t.n, 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
+            instr_desc(256, uniform(t.n), 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
         bool ok = true;
         for (int seg = 0; ok && seg < nseg; ++seg, ++j) {
           const int buf = j & 1;
-          ok = j < 2 || mbar_wait(tempty(buf), ((j >> 1) - 1) & 1);
+          ok = j < 2 || __all_sync(0xffffffffu, mbar_wait(tempty(buf), ((j >> 1) - 1) & 1));
           tc_fence_after();
-          const uint32_t d = tmem + buf * kTileN;
-          const int kb0 = (int)((long long)KB * seg / nseg), kb1 = (int)((long long)KB * (seg + 1) / nseg);
+          const uint32_t d = tmem_u + buf * kTileN;
+          const int kb0 = KB * seg / nseg, kb1 = KB * (seg + 1) / nseg;
           uint32_t accumulate = 0;
           for (int kb = kb0; ok && kb < kb1; ++kb, ++consumed) {
             const int s = consumed % kStages;
-            if (!mbar_wait(full(s), (consumed / kStages) & 1)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full(s), (consumed / kStages) & 1))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
-            const int ks = kWG ? min(4, (t.rows - kb * 64) >> 4) : 4;  // whole groups of this step
-#pragma unroll 4
-            for (int k = 0; k < ks; ++k) {
-              const uint64_t ad =
-                  kMmn ? sw128_mnmajor_desc(sa + k * 2048, kBoxBytes) : sw128_kmajor_desc(sa + k * 32);
-              const uint64_t bd =
-                  kNmn ? sw128_mnmajor_desc(sb + k * 2048, kBoxBytes) : sw128_kmajor_desc(sb + k * 32);
-              mma_pair(d, ad, bd, idesc, accumulate);
-              accumulate = 1;
+            const uint32_t sa = base_u + s * kStageBytes, sb = sa + kOpBytes;
+            const int ks = kWG ? min(4, (rows - kb * 64) >> 4) : 4;  // whole groups of this step
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t ad =
+                    kMmn ? sw128_mnmajor_desc(sa + k * 2048, kBoxBytes) : sw128_kmajor_desc(sa + k * 32);
+                const uint64_t bd =
+                    kNmn ? sw128_mnmajor_desc(sb + k * 2048, kBoxBytes) : sw128_kmajor_desc(sb + k * 32);
+                if (!kWG || k < ks) mma_pair(d, ad, bd, idesc, k > 0 ? 1u : accumulate);
+              }
+              commit_pair(empty(s));
             }
-            commit_pair(empty(s));
+            __syncwarp();
+            accumulate = 1;
           }
-          if (ok && seg == nseg - 1 && tail_rows(t)) {
+          if (ok && seg == nseg - 1 && tail) {
             const int b = n_tails & 1;
-            ok = wait_published(tail_ready(b), (n_tails >> 1) & 1);
+            ok = __all_sync(0xffffffffu, wait_published(tail_ready(b), (n_tails >> 1) & 1));
             ++n_tails;
             if (ok) {
               tc_fence_after();
               const uint32_t at = tails + b * kTailBytes;
-              mma_pair(d, sw128_mnmajor_desc(at, kTailBox), sw128_mnmajor_desc(at + 2 * kTailBox, kTailBox), idesc,
-                       accumulate);
-              commit_pair(tail_free(b));
+              if (elect_one()) {
+                mma_pair(d, sw128_mnmajor_desc(at, kTailBox), sw128_mnmajor_desc(at + 2 * kTailBox, kTailBox), idesc,
+                         accumulate);
+                commit_pair(tail_free(b));
+              }
+              __syncwarp();
             }
           }
-          commit_pair(tfull(buf));
+          if (elect_one()) commit_pair(tfull(buf));
+          __syncwarp();
         }
         if (!ok) {
-          *abort_flag = 1;
-          flag_status(a.status, MOE_DEV_TIMEOUT);
+          if (lane == 0) {
+            *abort_flag = 1;
+            flag_status(a.status, MOE_DEV_TIMEOUT);
+          }
           break;
         }
       }
