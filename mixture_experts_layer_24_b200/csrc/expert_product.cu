@@ -392,67 +392,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto tail_rows = [&](const Tile& t) { return kWG ? t.rows & 15 : 0; };
 
   if (warp == 4) {
-    // -------------------------------------------------------------- producer
-    if (lane == 0) {
-      int issued = 0, n_tails = 0;
-      Rows raw = ahead(cluster);
-      for (int tile = cluster; tile < total && !*abort_flag; tile += n_clusters) {
-        const Tile t = decode(tile, raw);
-        raw = ahead(tile + n_clusters);
-        const int KB = k_steps(t);
-        const int half = t.n / 2;  // this CTA's part of the N operand
-        const int mrow = t.m0 + (int)rank * 128;
-        if (tail_rows(t)) {
-          const int b = n_tails & 1;
-          if (n_tails >= 2 && !mbar_wait(tail_free(b), ((n_tails >> 1) - 1) & 1)) {
-            *abort_flag = 1;
-            flag_status(a.status, MOE_DEV_TIMEOUT);
-            break;
-          }
-          ++n_tails;
+    // -------------------------------------------------------------- producer (warp-uniform, as the MMA issuer below)
+    const int n_all = uniform(total);
+    int issued = 0, n_tails = 0;
+    bool ok = true;
+    Rows raw = ahead(cluster);
+    for (int tile = cluster; ok && tile < n_all && !uniform(*abort_flag); tile += n_clusters) {
+      const Tile t = decode(tile, raw);
+      raw = ahead(tile + n_clusters);
+      const int KB = uniform(k_steps(t)), tail = uniform(tail_rows(t));
+      const int half = uniform(t.n / 2);  // this CTA's part of the N operand
+      const int mrow = uniform(t.m0 + (int)rank * 128), ncol = uniform(t.n0 + (int)rank * half);
+      const int row0 = uniform(t.row0), wrow = uniform(t.e * (FORM == kForward ? a.m_total : a.k_total));
+      if (tail) {
+        const int b = n_tails & 1;
+        ok = n_tails < 2 || __all_sync(0xffffffffu, mbar_wait(tail_free(b), ((n_tails >> 1) - 1) & 1));
+        if (!ok) break;
+        ++n_tails;
+        if (elect_one()) {
           const uint32_t at = tails + b * kTailBytes, bar = map_rank(tail_landed(b), rank);
-          const int row = t.row0 + (t.rows & ~15);
+          const int row = row0 + (t.rows & ~15);
           mbar_arrive_expect_tx(tail_landed(b), (2 + half / 64) * kTailBox);
           tma_load_pair(at, &maps.n[2], bar, mrow, row);
           tma_load_pair(at + kTailBox, &maps.n[2], bar, mrow + 64, row);
           for (int j = 0; j < half / 64; ++j)
-            tma_load_pair(at + (2 + j) * kTailBox, &maps.n[1], bar, t.n0 + (int)rank * half + 64 * j, row);
+            tma_load_pair(at + (2 + j) * kTailBox, &maps.n[1], bar, ncol + 64 * j, row);
         }
-        // K-major N operand: one box of 16, 32, 64 or 128 rows
-        const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-        const uint32_t bytes = kOpBytes + (kNmn ? (uint32_t)(half / 64) * kBoxBytes : (16u << bi) * 128u);
-        for (int kb = 0; kb < KB; ++kb, ++issued) {
-          const int s = issued % kStages;
-          if (issued >= kStages && !mbar_wait(empty(s), ((issued / kStages) - 1) & 1)) {
-            *abort_flag = 1;
-            flag_status(a.status, MOE_DEV_TIMEOUT);
-            break;
-          }
-          const uint32_t sa = base + s * kStageBytes, sb = sa + kOpBytes;
+        __syncwarp();
+      }
+      // K-major N operand: one box of 16, 32, 64 or 128 rows
+      const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+      const uint32_t bytes = kOpBytes + (kNmn ? (uint32_t)(half / 64) * kBoxBytes : (16u << bi) * 128u);
+      for (int kb = 0; kb < KB; ++kb, ++issued) {
+        const int s = issued % kStages;
+        ok = issued < kStages || __all_sync(0xffffffffu, mbar_wait(empty(s), ((issued / kStages) - 1) & 1));
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t sa = base_u + s * kStageBytes, sb = sa + kOpBytes;
           const uint32_t bar = map_rank(full(s), 0);
           remote_expect_tx(bar, bytes);
           if (FORM == kForward) {
-            tma_load_pair(sa, &maps.m, bar, kb * 64, t.e * a.m_total + mrow);
+            tma_load_pair(sa, &maps.m, bar, kb * 64, wrow + mrow);
           } else {
-            const int row = kWG ? t.row0 + kb * 64 : t.e * a.k_total + kb * 64;
+            const int row = (kWG ? row0 : wrow) + kb * 64;
             tma_load_pair(sa, &maps.m, bar, mrow, row);
             tma_load_pair(sa + kBoxBytes, &maps.m, bar, mrow + 64, row);
           }
           if (kNmn) {
             for (int j = 0; j < half / 64; ++j)
-              tma_load_pair(sb + j * kBoxBytes, &maps.n[0], bar, t.n0 + (int)rank * half + 64 * j,
-                            t.row0 + kb * 64);
+              tma_load_pair(sb + j * kBoxBytes, &maps.n[0], bar, ncol + 64 * j, row0 + kb * 64);
           } else {
-            tma_load_pair(sb, &maps.n[bi], bar, kb * 64, t.row0 + (int)rank * half);
+            tma_load_pair(sb, &maps.n[bi], bar, kb * 64, row0 + ncol);
           }
         }
+        __syncwarp();
       }
-      // copies of the pair have landed before the leader goes on to the last cluster barrier
-      if (rank == 0)
-        for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
-          mbar_wait(full(g % kStages), (g / kStages) & 1);
-      for (int g = n_tails - 2 < 0 ? 0 : n_tails - 2; g < n_tails; ++g) mbar_wait(tail_landed(g & 1), (g >> 1) & 1);
     }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      flag_status(a.status, MOE_DEV_TIMEOUT);
+    }
+    // copies of the pair have landed before the leader goes on to the last cluster barrier
+    if (rank == 0)
+      for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
+        mbar_wait(full(g % kStages), (g / kStages) & 1);
+    for (int g = n_tails - 2 < 0 ? 0 : n_tails - 2; g < n_tails; ++g) mbar_wait(tail_landed(g & 1), (g >> 1) & 1);
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks the steps and one lane issues: warp-uniform code keeps descriptors in uniform registers,
