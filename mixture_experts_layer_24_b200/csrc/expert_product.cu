@@ -44,18 +44,21 @@
 // zero writer. Persistent; two TMEM accumulators of 256 columns, so a tile's
 // epilogue overlaps the next tile's MMAs. Every wait is bounded.
 //
-// Measured, 48 experts x 683 rows, 4096 x 4096 (1.1 TFLOP): forward and rows'
-// gradient 866 us cold (1270 TFLOP/s) and 900 to 1010 us under the power cap,
-// where cuBLAS' 8192^3 holds 1394; one expert x 32768 rows 879 us there (1251;
-// cuBLAS 1345). bf16 weights' gradient 930 us cold and 1150 capped, fp32 1060
-// and 1300 us (3.2 GB written). 333 rows: 251 us for the 1.6 GB of weights (98% of a copy's rate).
+// Measured under the power cap (990 W, the state of a training step), 4096 x
+// 4096: forward and rows' gradient of one expert x 32768 rows 814 us (1351
+// TFLOP/s; cuBLAS 1371), of 48 experts x 683 rows, with 1.6 GB of weights to
+// stream, 980 us (1122; 704 columns of MMA for 683 rows); fp32 weights' gradient
+// there 1290 us (3.2 GB written), bf16 1084 us. Not capped, 8 experts x 4096
+// rows: 692 us (1588) and 713 us. 333 rows: 246 us for the 1.6 GB of weights.
+//
 // What made the difference: expect_tx and waits without cluster-scope release
-// and acquire (1693 -> 916 us); whole sectors and TMA stores in the epilogue
-// (fp32 gradient 2154 -> 1207 us). What did not: bringing weights into L2
-// ahead (900 -> 995 us: the copies' issue rate is what it costs), eight
-// epilogue warps (no faster), 32-byte stores straight from the lanes (to 30%
-// slower with few rows per expert). Without its epilogue the rows' gradient
-// takes 837 us cold; the rest is the MMAs' power.
+// and acquire (1693 -> 916 us for 48 x 683 rows); whole sectors and TMA stores
+// in the epilogue (fp32 gradient 2154 -> 1207 us); warp-uniform issuing (8 x
+// 4096 rows 756 -> 692 us, their weights' gradient 835 -> 713 us). What did not:
+// bringing weights into L2 ahead (900 -> 995 us: the copies' issue rate is what
+// it costs), eight epilogue warps (no faster), 32-byte stores straight from the
+// lanes (to 30% slower with few rows per expert), nine smaller steps in flight
+// for few rows (no faster).
 #include <algorithm>
 
 #include "common.cuh"
@@ -70,8 +73,8 @@ constexpr int kTileN = 256;
 // K steps in flight: the weights' gradient gives one up for its tails and a third store box per warp.
 __host__ __device__ constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
 // N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost,
-// one expert of 32768 rows re-read its rows from HBM for every M tile (1166 us under the power cap; 879 us in bands of
-// 8, 864 in bands of 4; the weights' gradient is 1% faster in bands of 8).
+// one expert of 32768 rows re-read its rows from HBM for every M tile (then 1166 us under the power cap, 879 us in bands
+// of 8, 864 in bands of 4; the weights' gradient is 1% faster in bands of 8).
 constexpr int kBand = 8;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
