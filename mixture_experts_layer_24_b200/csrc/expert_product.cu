@@ -57,8 +57,11 @@
 // 4096 rows 756 -> 692 us, their weights' gradient 835 -> 713 us). What did not:
 // bringing weights into L2 ahead (900 -> 995 us: the copies' issue rate is what
 // it costs), eight epilogue warps (no faster), 32-byte stores straight from the
-// lanes (to 30% slower with few rows per expert), nine smaller steps in flight
-// for few rows (no faster).
+// lanes (to 30% slower with few rows per expert), coalesced stores from shared
+// memory instead of TMA stores and eviction hints on those (no faster), nine
+// smaller steps in flight for few rows (no faster). The weights' gradient is
+// held up by its writes: 12 experts x 683 rows in fp32 take 289 us, 209 without
+// the stores, 196 without the epilogue (tensor pipe 53% busy; forward 90%).
 #include <algorithm>
 
 #include "common.cuh"
