@@ -271,7 +271,7 @@ def test_swiglu_gradient_against_differences(layers):
 
 
 ROUTE = [(1, 1, 1, 128, 0.0), (1, 8, 384, 4096, 0.0), (37, 8, 384, 256, 0.0), (300, 2, 5, 2176, 0.2),
-         (65, 32, 40, 384, 0.1), (1025, 8, 64, 1024, 0.05), (2000, 1, 3, 128, 0.0)]
+         (65, 32, 40, 384, 0.1), (1025, 8, 64, 1024, 0.05), (2000, 1, 3, 128, 0.0), (600, 4, 1024, 128, 0.02)]
 
 
 @pytest.mark.parametrize("T,K,E,H,drop", ROUTE)
@@ -309,7 +309,7 @@ def _segments(counts, slack=0):
 PROD = [([1], 0, 128, 128), ([0, 1, 0, 0], 3, 128, 256), ([17, 0, 64, 63, 65], 5, 256, 384),
         ([256, 257, 511], 0, 384, 128), ([300, 2, 0, 33], 40, 640, 512), ([0, 0, 0], 2, 256, 128),
         ([15, 16, 31, 32, 33, 47, 48, 49, 127, 128, 129, 191, 193], 1, 256, 512), ([1] * 70, 0, 512, 256),
-        ([0] * 40 + [700] + [3] * 8, 9, 2048, 1152)]
+        ([0] * 40 + [700] + [3] * 8, 9, 2048, 1152), ([1, 0, 2, 0] * 256, 3, 128, 128)]
 
 
 def _ints(seed, *shape):
@@ -629,6 +629,66 @@ def test_activation_and_products_past_32_bit_offsets(layers):
     for e in (0, E - 1):
         assert torch.equal(dw[e], dy[e][:, None] * a[e][None, :])
     assert L.status() == 0
+
+
+def test_calls_from_two_threads(layers):
+    """Two host threads, each with a stream of its own, on one layer: the bits of a single thread."""
+    import threading
+    T, K, E, H, I = 65, 4, 16, 512, 256
+    L, r = layers(H, E, K, I), _cuda(R.routing(T, K, E, 90))
+    w = _rand(91, E, 2 * I, H, std=0.05)
+    sets = [(_rand(92 + s, T, H), _rand(94 + s, T, K, dtype=F32)) for s in range(2)]
+
+    def work(s):
+        x, dw = sets[s]
+        xs = L.dispatch(x, r["inv"])
+        h, q, sc = L.swiglu_ckpt(L.expert_product(xs, w, r["offsets"]), r["inv"])
+        return [xs, h, q, sc, L.expert_wgrad(L.swiglu_ckpt_bwd(q, sc, h, r["w"], r["inv"])[0], xs, r["offsets"]),
+                *L.route_bwd(x, r["w"], dw, r["offsets"], r["perm_src"], r["perm_k"])]
+
+    want = [work(s) for s in range(2)]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def run(s):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[s] = work(s)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # surfaced below
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(s,)) for s in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(timeout=120)
+    assert not errors, errors
+    for s in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[s], want[s]))
+    assert L.status() == 0
+
+
+def test_launches_are_counted_and_timed(layers):
+    """moe_launch_count and moe_profile_* see the training calls under their own kinds."""
+    import mixture_experts_layer_24_b200 as M
+    T, K, E, H, I = 9, 2, 8, 256, 128
+    L, r = layers(H, E, K, I), _cuda(R.routing(T, K, E, 96))
+    x, w = _rand(97, T, H), _rand(98, E, 2 * I, H)
+    torch.cuda.synchronize()
+    before = L.launches()
+    M.moe_profile_enable(L.ctx, True)
+    M.moe_profile_read(L.ctx)
+    xs = L.dispatch(x, r["inv"])
+    h, q, s = L.swiglu_ckpt(L.expert_product(xs, w, r["offsets"]), r["inv"])
+    L.expert_wgrad(q.to(BF16), xs, r["offsets"])
+    L.route_bwd(x, r["w"], r["w"], r["offsets"], r["perm_src"], r["perm_k"])
+    prof = M.moe_profile_read(L.ctx)
+    M.moe_profile_enable(L.ctx, False)
+    assert L.launches() - before == 1 + 1 + 1 + 1 + 2
+    assert [prof[k][1] for k in ("rows", "swiglu", "route_bwd", "product")] == [1, 1, 1, 2]
+    assert all(prof[k][0] > 0 for k in ("rows", "swiglu", "route_bwd", "product")) and prof["router"][1] == 0
 
 
 STEP = [(1, 256, 8, 2, 128), (37, 256, 8, 2, 256), (300, 512, 48, 4, 256)]
