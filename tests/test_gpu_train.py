@@ -631,6 +631,19 @@ def test_activation_and_products_past_32_bit_offsets(layers):
     assert L.status() == 0
 
 
+def test_router_gradient_in_plain_stream_order(layers):
+    """Without programmatic dependent launch: the same bits."""
+    import mixture_experts_layer_24_b200 as M
+    T, K, E, H = 700, 4, 12, 256
+    r = _cuda(R.routing(T, K, E, 99, 0.05))
+    args = (_rand(100, T, H), r["w"], _rand(101, T, K, dtype=F32), r["offsets"], r["perm_src"], r["perm_k"])
+    plain = M.MoeLayer(H, E, K, 128, flags=M.binding.MOE_FLAG_NO_PDL)
+    for _ in range(3):
+        got, want = plain.route_bwd(*args), layers(H, E, K).route_bwd(*args)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    plain.close()
+
+
 def test_calls_from_two_threads(layers):
     """Two host threads, each with a stream of its own, on one layer: the bits of a single thread."""
     import threading
