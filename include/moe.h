@@ -387,7 +387,7 @@ moe_status_t moe_swiglu_ckpt(moe_ctx_t* ctx, const void* gu, const int32_t* inv,
  * w h (NULL: not wanted). dh is then the gradient before the weight: dout
  * through the down product, unweighted; hw is what dout multiplies in the down
  * weights' gradient. Without topk_w, w = 1 and hw, dtopk_w are NULL; topk_w
- * needs inv, or rows in pair order. */
+ * needs inv, or rows in pair order. A pair's bits depend on its own row alone. */
 moe_status_t moe_swiglu_ckpt_bwd(moe_ctx_t* ctx, const uint8_t* q, const float* s, const void* dh,
                                  const float* topk_w, const int32_t* inv, int rows, void* dgu, void* hw,
                                  float* dtopk_w, moe_stream_t stream);

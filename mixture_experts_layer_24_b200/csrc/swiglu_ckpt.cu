@@ -132,8 +132,12 @@ __global__ void __launch_bounds__(256, 5) swiglu_ckpt_kernel(const uint4* __rest
   }
 }
 
+constexpr int kMaxBlocks = 64;  // of a row: I <= 8192
+
 // kWarps warps per row; each half-warp takes every (2 kWarps)-th 128-column
-// block, two blocks' loads in flight.
+// block, two blocks' loads in flight. The weight's gradient is summed per block
+// and then over the blocks, in an order that does not depend on kWarps: a
+// pair's bits are the same among any number of rows.
 template <bool kWeighted, int kWarps>
 __global__ void __launch_bounds__(256, 4) swiglu_ckpt_bwd_kernel(const uint2* __restrict__ q,
                                                                const float* __restrict__ s,
@@ -143,19 +147,18 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_bwd_kernel(const uint2* __
                                                                uint4* __restrict__ dgu, uint4* __restrict__ hw,
                                                                float* __restrict__ dw, int* status) {
   constexpr int kRows = 8 / kWarps;  // rows per CTA
-  __shared__ float s_dot[8];
+  __shared__ float s_dot[kRows][kMaxBlocks];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15;
   const long long i = (long long)blockIdx.x * kRows + warp / kWarps;
   const bool in = i < rows;
   const int r = !in ? -1 : inv ? pair_row(inv, i, rows, status) : (int)i;
-  float dot = 0.0f;
   if (r >= 0) {
     const float wk = kWeighted ? __ldg(w + i) : 1.0f;
     constexpr int kStep = 2 * kWarps;
     for (int b0 = (warp % kWarps) * 2 + (lane >> 4); b0 < blocks; b0 += 2 * kStep) {
       uint2 qg[2], qu[2];
       uint4 dv[2];
-      float sg[2], su[2];
+      float sg[2], su[2], dot[2] = {};
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const int b = b0 + n * kStep;
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_bwd_kernel(const uint2* __
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float sig = sigmoid(g[j]), silu = g[j] * sig, hj = silu * u[j];
-          if (kWeighted) dot = fmaf(d[j], hj, dot);
+          if (kWeighted) dot[n] = fmaf(d[j], hj, dot[n]);
           o[j] = wk * hj;
           const float wd = wk * d[j];
           const float dgj = wd * u[j] * sig * (1.0f + g[j] * (1.0f - sig));
@@ -190,20 +193,27 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_bwd_kernel(const uint2* __
         dgu[gv + blocks * 16] = RowBf16::pack(u);
         if (kWeighted && hw) hw[hv] = RowBf16::pack(o);
       }
+      if (kWeighted) {  // lanes 0-7 of the half-warp take the first block's sum, 8-15 the second's
+        const unsigned half = 0xffffu << (lane & 16);
+        const bool second = l >= 8;
+        float sum = (second ? dot[1] : dot[0]) + __shfl_xor_sync(half, second ? dot[0] : dot[1], 8);
+#pragma unroll
+        for (int x = 4; x >= 1; x >>= 1) sum += __shfl_xor_sync(half, sum, x);
+        const int b = b0 + (second ? kStep : 0);
+        if ((l & 7) == 0 && b < blocks) s_dot[warp / kWarps][b] = sum;
+      }
     }
   }
   if (kWeighted) {
+    if (kWarps > 1) __syncthreads();
+    else __syncwarp();
+    if (!in || warp % kWarps) return;
+    float sum = 0.0f;
+    if (r >= 0)
+      for (int b = lane; b < blocks; b += 32) sum += s_dot[warp / kWarps][b];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (kWarps > 1) {  // the sums of the row's warps, in warp order
-      if (lane == 0) s_dot[warp] = dot;
-      __syncthreads();
-      const int w0 = warp / kWarps * kWarps;
-      dot = s_dot[w0];
-#pragma unroll
-      for (int n = 1; n < kWarps; ++n) dot += s_dot[w0 + n];
-    }
-    if (in && lane == 0 && warp % kWarps == 0) dw[i] = r >= 0 ? dot : 0.0f;
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) dw[i] = sum;
   }
 }
 

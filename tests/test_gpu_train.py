@@ -246,6 +246,22 @@ def test_swiglu_ckpt_bwd(layers, T, K, I, drop, weighted):
     assert (dw[~kept] == 0).all()
 
 
+@pytest.mark.parametrize("I", [128, 640, 2048, 8192])
+def test_swiglu_rows_do_not_depend_on_each_other(layers, I):
+    """A pair's codes, gradients and weight's gradient have the same bits alone, among few and among many."""
+    L, rows = layers(128, 8, 1, I), 9000
+    inv = torch.arange(rows, dtype=torch.int32, device="cuda").view(-1, 1)
+    gu, dh, w = _gate_up(31, rows, I), _rand(32, rows, I), _rand(33, rows, 1, dtype=F32)
+    h, q, s = L.swiglu_ckpt(gu, inv)
+    many = (h, q, s) + L.swiglu_ckpt_bwd(q, s, dh, topk_w=w, inv=inv)
+    for lo, hi in ((0, 1), (3, 40), (100, 1900), (4000, 7000)):
+        few = L.swiglu_ckpt(gu[lo:hi].contiguous(), inv[:hi - lo])
+        few += L.swiglu_ckpt_bwd(q[lo:hi].contiguous(), s[lo:hi].contiguous(), dh[lo:hi].contiguous(),
+                                 topk_w=w[lo:hi].contiguous(), inv=inv[:hi - lo])
+        for a, b in zip(few, many):
+            assert torch.equal(a, b[lo:hi])
+
+
 def test_swiglu_gradient_against_differences(layers):
     """dgu (fp32 reference of the same formula aside) against central differences of silu(g) u in 64 bits at the
     checkpoint's values."""
