@@ -19,12 +19,13 @@
 //
 // Measured at 4096 tokens, K = 8, H = 4096, bf16, of a copy's 6.56 TB/s:
 // dispatch 49 us (95%), combine 44 us (104%: part of the rows is still in L2),
-// its gradient 89 us (98%), dispatch gradient 44 us (104%), with the router's
-// term 66 us: that term reads K fp32 router rows per token, 537 MB, which come
-// from L1 and L2. Expert rows are read past L1 (they are read once), which
-// leaves it to the router rows of the busiest experts: 105 us before. A CTA
-// that keeps 64 columns of the whole router weight in shared memory and passes
-// the tokens by it took 126 to 174 us.
+// its gradient 89 us (98%), dispatch gradient 44 us (104%). With the router's
+// term that takes 68 us from a cold L2 (55 us without it): K fp32 router rows
+// per token, 537 MB, come from L1 and L2. Expert rows are read past L1 (they
+// are read once), which leaves it to the router rows of the busiest experts:
+// 105 us before. A CTA that keeps 64 columns of the whole router weight in
+// shared memory and passes the tokens by it took 126 to 174 us; expert rows
+// requested before or together with the router rows 71 to 82 us (registers).
 #include "rows.cuh"
 #include "train.h"
 
@@ -32,10 +33,15 @@ namespace moe {
 
 namespace {
 
-// Rows in flight per thread: expert rows, and router rows. Few, so that five blocks fit an SM: with eight expert rows
-// (64 registers, four blocks) the combine took 53 us and the gradient with the router's term 70 us.
+// Expert rows in flight per thread. Few, so that five blocks fit an SM: with eight (64 registers, four blocks) the
+// combine took 53 us.
 constexpr int kSlots = 4;
-constexpr int kRouterSlots = 2;
+// 16-byte pieces of a row that the router's form takes of every token before it goes on to the next ones: the router
+// rows' columns in use stay in L1.
+constexpr unsigned kSlice = 64;
+
+// The sums of gather_sum_kernel.
+enum Sum { kPlain, kWeighted, kRouter };
 
 // One thread per 16-byte piece of the output row.
 template <class R, bool kCkpt>
@@ -70,8 +76,15 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
   return v;
 }
 
-// acc += the sum over k of a token's rows, one 16-byte piece of them: f or, kWeighted, w f.
-template <class R, bool kWeighted>
+__device__ __forceinline__ uint2 load_once(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// acc += the sum over k of a token's rows, one 16-byte piece of them (kHalves: two 8-byte pieces, v and v + 16): f or,
+// with weights, w f.
+template <class R, bool kWeights, bool kHalves>
 __device__ __forceinline__ void sum_rows(const uint4* __restrict__ rows, const float* __restrict__ w,
                                          const int32_t* __restrict__ inv, size_t t, int K, int P, unsigned V,
                                          unsigned v, float (&acc)[R::kN], int* status) {
@@ -82,18 +95,26 @@ __device__ __forceinline__ void sum_rows(const uint4* __restrict__ rows, const f
 #pragma unroll
     for (int u = 0; u < kSlots; ++u) {
       p[u] = k0 + u < K ? pair_row(inv, (long long)t * K + k0 + u, P, status) : -1;
-      wk[u] = kWeighted && k0 + u < K ? __ldg(w + t * K + k0 + u) : 1.0f;
+      wk[u] = kWeights && k0 + u < K ? __ldg(w + t * K + k0 + u) : 1.0f;
     }
 #pragma unroll
     for (int u = 0; u < kSlots; ++u)
-      if (p[u] >= 0) a[u] = load_once(rows + (size_t)p[u] * V + v);
+      if (p[u] >= 0) {
+        if (kHalves) {
+          const uint2* r = reinterpret_cast<const uint2*>(rows + (size_t)p[u] * V) + v;
+          const uint2 lo = load_once(r), hi = load_once(r + 16);
+          a[u] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+          a[u] = load_once(rows + (size_t)p[u] * V + v);
+        }
+      }
 #pragma unroll
     for (int u = 0; u < kSlots; ++u) {
       if (p[u] < 0) continue;
       float f[R::kN];
       R::unpack(a[u], f);
 #pragma unroll
-      for (int j = 0; j < R::kN; ++j) acc[j] = kWeighted ? fmaf(wk[u], f[j], acc[j]) : acc[j] + f[j];
+      for (int j = 0; j < R::kN; ++j) acc[j] = kWeights ? fmaf(wk[u], f[j], acc[j]) : acc[j] + f[j];
     }
   }
 }
@@ -110,48 +131,69 @@ __device__ __forceinline__ void add_router(float (&acc)[kN], float d, const floa
   }
 }
 
-// kWeighted: out = sum_k w y (the combine). Otherwise the dispatch's gradient,
-// with the router's term when dl is given.
-template <class R, bool kWeighted>
-__global__ void __launch_bounds__(256, 5) gather_sum_kernel(const uint4* __restrict__ rows,
-                                                             const float* __restrict__ w,
-                                                             const int32_t* __restrict__ inv,
-                                                             const float* __restrict__ dl,
-                                                             const int32_t* __restrict__ idx,
-                                                             const float* __restrict__ wr, int T, int K, int E,
-                                                             unsigned V, uint4* __restrict__ out, int* status) {
+// kWeighted: out = sum_k w y (the combine). Otherwise the dispatch's gradient, kRouter: with the router's term.
+//
+// Router rows are fp32: where expert rows are bf16, a thread takes columns 4l..4l+3 of both halves of a 128-column block
+// in place of eight neighbouring ones, so that a warp's loads of router rows are contiguous too (77.7 -> 73.3 us for
+// 4096 tokens of 8 x 4096; slices and one router row at a time, which lets six blocks fit an SM: 67.7 us).
+template <class R, Sum kSum>
+__global__ void __launch_bounds__(256, kSum == kRouter && R::kN == 8 ? 6 : 5)
+    gather_sum_kernel(const uint4* __restrict__ rows, const float* __restrict__ w, const int32_t* __restrict__ inv,
+                      const float* __restrict__ dl, const int32_t* __restrict__ idx, const float* __restrict__ wr,
+                      int T, int K, int E, unsigned V, uint4* __restrict__ out, int* status) {
+  constexpr bool kHalves = kSum == kRouter && R::kN == 8;
   const unsigned i = blockIdx.x * 256u + threadIdx.x;
-  const unsigned t = i / V, v = i - t * V;
+  unsigned t, v;
+  if (kSum == kRouter) {
+    const unsigned slice = i / (kSlice * T), v0 = slice * kSlice;
+    if (v0 >= V) return;
+    const unsigned width = min(kSlice, V - v0), j = i - v0 * T;
+    t = j / width;
+    v = v0 + (j - t * width);
+    if (kHalves) v = v / 16 * 32 + v % 16;  // 8-byte pieces
+  } else {
+    t = i / V;
+    v = i - t * V;
+  }
   if (t >= (unsigned)T) return;
   float acc[R::kN] = {};
-  if (!kWeighted && dl) {
+  if (kSum == kRouter) {
     const size_t H = (size_t)V * R::kN;
-    for (int k0 = 0; k0 < K; k0 += kRouterSlots) {
-      int e[kRouterSlots];
-      float d[kRouterSlots];
+    constexpr int kSlotsR = kHalves ? 1 : 2;  // router rows in flight
+    for (int k0 = 0; k0 < K; k0 += kSlotsR) {
+      int e[kSlotsR];
+      float d[kSlotsR];
 #pragma unroll
-      for (int u = 0; u < kRouterSlots; ++u) {
+      for (int u = 0; u < kSlotsR; ++u) {
         const bool in = k0 + u < K;
         e[u] = in ? __ldg(idx + (size_t)t * K + k0 + u) : 0;
         d[u] = in ? __ldg(dl + (size_t)t * K + k0 + u) : 0.0f;
       }
-      float4 q[kRouterSlots][R::kN / 4];
+      float4 q[kSlotsR][R::kN / 4];
 #pragma unroll
-      for (int u = 0; u < kRouterSlots; ++u) {
+      for (int u = 0; u < kSlotsR; ++u) {
         const bool good = e[u] >= 0 && e[u] < E;
         if (!good) flag_status(status, MOE_DEV_BAD_EXPERT);
         if (!good || k0 + u >= K) e[u] = -1;
 #pragma unroll
         for (int j = 0; j < R::kN / 4; ++j)
-          if (e[u] >= 0) q[u][j] = __ldg(reinterpret_cast<const float4*>(wr + e[u] * H + v * R::kN) + j);
+          if (e[u] >= 0) q[u][j] = __ldg(reinterpret_cast<const float4*>(wr + e[u] * H) + v + 16 * j);
       }
 #pragma unroll
-      for (int u = 0; u < kRouterSlots; ++u)
+      for (int u = 0; u < kSlotsR; ++u)
         if (e[u] >= 0) add_router(acc, d[u], q[u]);
     }
   }
-  sum_rows<R, kWeighted>(rows, w, inv, t, K, T * K, V, v, acc, status);
-  out[(size_t)t * V + v] = R::pack(acc);
+  sum_rows<R, kSum == kWeighted, kHalves>(rows, w, inv, t, K, T * K, V, v, acc, status);
+  const uint4 sum = R::pack(acc);
+  uint4* o = out + (size_t)t * V;
+  if (kHalves) {
+    uint2* h = reinterpret_cast<uint2*>(o) + v;
+    h[0] = make_uint2(sum.x, sum.y);
+    h[16] = make_uint2(sum.z, sum.w);
+  } else {
+    o[v] = sum;
+  }
 }
 
 // One warp per pair.
@@ -225,10 +267,9 @@ cudaError_t launch_dispatch_bwd(const void* rows, int dtype, const int32_t* inv,
   const bool f32 = dtype == MOE_T_F32;
   const unsigned V = (unsigned)(f32 ? H / 4 : H / 8);
   const unsigned blocks = blocks_for((long long)T * V);
-  if (f32)
-    gather_sum_kernel<RowF32, false><<<blocks, 256, 0, s>>>(r, nullptr, inv, dl, idx, wr, T, K, E, V, o, status);
-  else
-    gather_sum_kernel<RowBf16, false><<<blocks, 256, 0, s>>>(r, nullptr, inv, dl, idx, wr, T, K, E, V, o, status);
+  auto sum = dl ? (f32 ? gather_sum_kernel<RowF32, kRouter> : gather_sum_kernel<RowBf16, kRouter>)
+                : (f32 ? gather_sum_kernel<RowF32, kPlain> : gather_sum_kernel<RowBf16, kPlain>);
+  sum<<<blocks, 256, 0, s>>>(r, nullptr, inv, dl, idx, wr, T, K, E, V, o, status);
   return cudaGetLastError();
 }
 
@@ -239,9 +280,9 @@ cudaError_t launch_combine_weighted(const void* y, int dtype, const float* w, co
   const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
   const unsigned blocks = blocks_for((long long)T * V);
   if (dtype == MOE_T_F32)
-    gather_sum_kernel<RowF32, true><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o, status);
+    gather_sum_kernel<RowF32, kWeighted><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o, status);
   else
-    gather_sum_kernel<RowBf16, true><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o,
+    gather_sum_kernel<RowBf16, kWeighted><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o,
                                                             status);
   return cudaGetLastError();
 }
