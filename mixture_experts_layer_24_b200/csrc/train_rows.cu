@@ -25,7 +25,8 @@
 // are read once), which leaves it to the router rows of the busiest experts:
 // 105 us before. A CTA that keeps 64 columns of the whole router weight in
 // shared memory and passes the tokens by it took 126 to 174 us; expert rows
-// requested before or together with the router rows 71 to 82 us (registers).
+// requested before or together with the router rows 71 to 82 us (registers);
+// paired fp32 instructions in both sums changed nothing.
 #include "rows.cuh"
 #include "train.h"
 
