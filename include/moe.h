@@ -320,9 +320,10 @@ moe_status_t moe_plan_hot_set(const int64_t* hist, int E, int n_hot, int32_t* ho
  * The pieces of one training step of the layer: tokens to expert order and
  * back, the experts' activation with 8-bit checkpoints, the experts' products,
  * and the gradient of each. Pair i = t*K + k; inv[i] (moe_permute) is its row
- * in expert order, in [0, T*K), or negative for a dropped pair, which takes no
- * part: its token's sum leaves it out, its weight's gradient is 0, and rows
- * behind the last kept pair are neither read nor written. The kept entries of
+ * in expert order, in [0, T*K), or negative for a dropped pair, which has no
+ * row: its token's sum leaves it out, its weight's gradient is 0, and rows
+ * behind the last kept pair are neither read nor written. (Its logit is still
+ * one of the softmax's: moe_route_bwd_topk.) The kept entries of
  * inv name distinct rows. An index outside its array is ignored (as a dropped
  * pair) and sets MOE_DEV_BAD_INDEX.
  * Rows are contiguous, of the context's H or I columns unless stated, and
@@ -349,10 +350,12 @@ moe_status_t moe_dispatch(moe_ctx_t* ctx, const void* x, const float* x_scales, 
 
 /* Gradient of the dispatch, and of the router's input where dlogit is given:
  *   dx[t, :] = sum_k dlogit[t, k] * w_router[topk_idx[t, k], :] + sum_k dx_sorted[inv[t*K+k], :]
- * in this order in fp32, k ascending, rounded once.
+ * in this order in fp32, k ascending, rounded once. The first sum takes every
+ * k, the second the kept pairs.
  *   dx_sorted [T*K, H], dx [T, H], both bf16 or both fp32; dlogit [T, K] fp32
- *   (moe_route_bwd), topk_idx [T, K], w_router [E, H] fp32: all three, or all
- *   NULL. A topk_idx outside [0, E) adds nothing and sets MOE_DEV_BAD_EXPERT. */
+ *   (moe_route_bwd), topk_idx [T, K] (moe_route's choice, of dropped pairs too),
+ *   w_router [E, H] fp32: all three, or all NULL. A topk_idx outside [0, E) adds
+ *   nothing and sets MOE_DEV_BAD_EXPERT. */
 moe_status_t moe_dispatch_bwd(moe_ctx_t* ctx, const void* dx_sorted, int dtype, const int32_t* inv,
                               const float* dlogit, const int32_t* topk_idx, const float* w_router, int T, void* dx,
                               moe_stream_t stream);
@@ -397,17 +400,31 @@ size_t moe_route_bwd_workspace_size(const moe_ctx_t* ctx, int T);
 
 /* Gradient of moe_route through the weights (the choice of experts has none):
  *   dlogit[t, k] = topk_w[t, k] * (dtopk_w[t, k] - sum_j topk_w[t, j] dtopk_w[t, j])
- *   dw_router[e, :] = sum over the kept pairs (t, k) of expert e of dlogit[t, k] * x[t, :]
+ *   dw_router[e, :] = sum over the listed pairs (t, k) of expert e of dlogit[t, k] * x[t, :]
  *   dlogit_bias[e]  = sum over the same pairs of dlogit[t, k]       (NULL: not wanted)
  *   x [T, H] bf16 with x_scales NULL, or e4m3 codes with x_scales [T, H/128]
  *   (x = code * scale); topk_w, dtopk_w, dlogit [T, K] fp32; offsets, perm_src,
- *   perm_k from moe_permute; dw_router [E, H] fp32, dlogit_bias [E] fp32, both
+ *   perm_k: the list of pairs, moe_permute of the topk_idx that moe_route chose;
+ *   dw_router [E, H] fp32, dlogit_bias [E] fp32, both
  *   written whole (zeros for experts without pairs). ws: 256-byte aligned;
- *   calls that may overlap need workspaces of their own. */
+ *   calls that may overlap need workspaces of their own.
+ * The weights are a softmax over all K chosen logits, so a dropped pair's logit
+ * has a gradient too (its dtopk_w is 0, its dlogit is not). The list of a
+ * forward that dropped pairs leaves them out, and their share of dw_router and
+ * dlogit_bias with them: there, call moe_route_bwd_topk. */
 moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales, const float* topk_w,
                            const float* dtopk_w, const int32_t* offsets, const int32_t* perm_src,
                            const int32_t* perm_k, int T, float* dlogit, float* dw_router, float* dlogit_bias, void* ws,
                            size_t ws_bytes, moe_stream_t stream);
+
+/* The same from moe_route's choice topk_idx [T, K] in place of a list of pairs,
+ * which this call makes itself: the sums take every pair, dropped or not. A
+ * topk_idx outside [0, E) sets MOE_DEV_BAD_EXPERT; its pair adds nothing (give
+ * the choice as moe_route wrote it, not with dropped pairs marked in it). */
+size_t moe_route_bwd_topk_workspace_size(const moe_ctx_t* ctx, int T);
+moe_status_t moe_route_bwd_topk(moe_ctx_t* ctx, const void* x, const float* x_scales, const int32_t* topk_idx,
+                                const float* topk_w, const float* dtopk_w, int T, float* dlogit, float* dw_router,
+                                float* dlogit_bias, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* One product per expert over its sorted rows p = offsets[e] .. offsets[e+1]-1
  * (tensor cores, fp32 accumulation, one rounding), w [E, n_out, n_in] bf16:

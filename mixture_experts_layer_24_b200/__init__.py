@@ -59,6 +59,8 @@ from .binding import (  # noqa: F401
     moe_quantize_mx,
     moe_route,
     moe_route_bwd,
+    moe_route_bwd_topk,
+    moe_route_bwd_topk_workspace_size,
     moe_route_bwd_workspace_size,
     moe_route_noalloc,
     moe_slots_create,

@@ -43,7 +43,8 @@ EXPORTS = ["moe_ctx_create", "moe_ctx_destroy", "moe_workspace_size", "moe_route
            "moe_debug_wait_flag", "moe_ep_pack", "moe_ep_recv_plan", "moe_ep_gather_rows", "moe_quantize_mx",
            "moe_debug_fail_allocs", "moe_dispatch", "moe_dispatch_bwd", "moe_combine_weighted",
            "moe_combine_weighted_bwd", "moe_swiglu_ckpt", "moe_swiglu_ckpt_bwd", "moe_route_bwd_workspace_size",
-           "moe_route_bwd", "moe_expert_product", "moe_expert_wgrad"]
+           "moe_route_bwd", "moe_route_bwd_topk_workspace_size", "moe_route_bwd_topk", "moe_expert_product",
+           "moe_expert_wgrad"]
 
 PROF_KINDS = ["router", "topk", "permute", "gather", "gate_up", "down", "quant", "combine", "ffn_fused", "rows",
               "swiglu", "route_bwd", "product"]
@@ -115,6 +116,8 @@ def lib():
         "moe_swiglu_ckpt_bwd": ([P, P, P, P, P, P, I, P, P, P, P], S),
         "moe_route_bwd_workspace_size": ([P, I], Z),
         "moe_route_bwd": ([P, P, P, P, P, P, P, P, I, P, P, P, P, Z, P], S),
+        "moe_route_bwd_topk_workspace_size": ([P, I], Z),
+        "moe_route_bwd_topk": ([P, P, P, P, P, P, I, P, P, P, P, Z, P], S),
         "moe_expert_product": ([P, P, P, P, I, I, I, I, P, P], S),
         "moe_expert_wgrad": ([P, P, P, P, I, I, I, I, I, P, P], S),
     }
@@ -263,6 +266,17 @@ def moe_route_bwd(ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, 
     _check(lib().moe_route_bwd(ctx, _p(x), _p(x_scales), _p(topk_w), _p(dtopk_w), _p(offsets), _p(perm_src),
                                _p(perm_k), T, _p(dlogit), _p(dw_router), _p(dlogit_bias), _p(ws), _nbytes(ws),
                                _s(stream)), "moe_route_bwd")
+
+
+def moe_route_bwd_topk_workspace_size(ctx, T: int) -> int:
+    return int(lib().moe_route_bwd_topk_workspace_size(ctx, T))
+
+
+def moe_route_bwd_topk(ctx, x, x_scales, topk_idx, topk_w, dtopk_w, T, dlogit, dw_router, dlogit_bias, ws,
+                       stream=None):
+    _check(lib().moe_route_bwd_topk(ctx, _p(x), _p(x_scales), _p(topk_idx), _p(topk_w), _p(dtopk_w), T, _p(dlogit),
+                                    _p(dw_router), _p(dlogit_bias), _p(ws), _nbytes(ws), _s(stream)),
+           "moe_route_bwd_topk")
 
 
 def moe_expert_product(ctx, a, w, offsets, P, n_in, n_out, transposed, out, stream=None):
@@ -669,13 +683,16 @@ class MoeLayer:
         moe_swiglu_ckpt_bwd(self.ctx, q, s, dh, topk_w, inv, rows, dgu, hw, dw, self._stream())
         return dgu, hw, dw
 
-    def route_bwd(self, x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales=None, stream=None):
+    def route_bwd(self, x, topk_w, dtopk_w, offsets=None, perm_src=None, perm_k=None, x_scales=None, stream=None,
+                  topk_idx=None):
         """(dlogit [T, K], dw_router [E, H], dlogit_bias [E]), all fp32: the gradient of ``route`` through its
-        weights; offsets, perm_src and perm_k are ``permute``'s. x is bf16, or the e4m3 codes (uint8) of its checkpoint
-        with x_scales [T, H/128]."""
+        weights. offsets, perm_src and perm_k are ``permute``'s for the topk_idx that ``route`` chose. Where the forward
+        dropped pairs, its own list leaves them out, although their logits are in the softmax: give topk_idx [T, K],
+        ``route``'s choice, in place of the three. x is bf16, or the e4m3 codes (uint8) of its checkpoint with
+        x_scales [T, H/128]."""
         if self._elsewhere(stream):
             with self._on(stream):
-                return self.route_bwd(x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales)
+                return self.route_bwd(x, topk_w, dtopk_w, offsets, perm_src, perm_k, x_scales, None, topk_idx)
         T = _rows(x, "x")
         P = T * self.K
         _want(x, "x", torch.bfloat16 if x_scales is None else torch.uint8, (T, self.H), self.device)
@@ -683,13 +700,22 @@ class MoeLayer:
             _want(x_scales, "x_scales", torch.float32, (T, self.H // 128), self.device)
         _want(topk_w, "topk_w", torch.float32, (T, self.K), self.device)
         _want(dtopk_w, "dtopk_w", torch.float32, (T, self.K), self.device)
-        _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
-        _want(perm_src, "perm_src", torch.int32, (P,), self.device)
-        _want(perm_k, "perm_k", torch.int32, (P,), self.device)
-        ws = x.new_empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8)
+        if topk_idx is not None:
+            if offsets is not None or perm_src is not None or perm_k is not None:
+                raise ValueError("topk_idx: in place of offsets, perm_src and perm_k")
+            _want(topk_idx, "topk_idx", torch.int32, (T, self.K), self.device)
+            ws = x.new_empty(moe_route_bwd_topk_workspace_size(self.ctx, T), dtype=torch.uint8)
+        else:
+            _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+            _want(perm_src, "perm_src", torch.int32, (P,), self.device)
+            _want(perm_k, "perm_k", torch.int32, (P,), self.device)
+            ws = x.new_empty(moe_route_bwd_workspace_size(self.ctx, T), dtype=torch.uint8)
         dl = torch.empty_like(topk_w)
         dwr = topk_w.new_empty((self.E, self.H))
         db = topk_w.new_empty(self.E)
+        if topk_idx is not None:
+            moe_route_bwd_topk(self.ctx, x, x_scales, topk_idx, topk_w, dtopk_w, T, dl, dwr, db, ws, self._stream())
+            return dl, dwr, db
         moe_route_bwd(self.ctx, x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, dl, dwr, db, ws,
                       self._stream())
         return dl, dwr, db

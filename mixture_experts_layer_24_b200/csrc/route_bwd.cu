@@ -3,9 +3,12 @@
 //   dl[t,k]   = w[t,k] * (dw[t,k] - sum_j w[t,j] dw[t,j])
 //   dWr[e, :] = sum over the pairs (t,k) of expert e of dl[t,k] * x[t, :]
 //   dbias[e]  = sum over the same pairs of dl[t,k]
-// (logits outside the top k get no gradient). Sums are fp32.
+// (logits outside the top k get no gradient). Sums are fp32. A pair that the
+// forward dropped has dw = 0 and a dl all the same, so the sums are over every
+// chosen pair: the list of pairs has to be the sort of the router's own choice
+// (moe_route_bwd_topk makes it), not that of the kept pairs.
 //
-// The pairs are already sorted by expert, so dWr is a segmented sum of scaled
+// The pairs come sorted by expert, so dWr is a segmented sum of scaled
 // rows: the sorted list is cut every `chunk` pairs, a CTA takes one piece and
 // 2048 columns, and adds up each expert's run inside it. A run that is its
 // expert's whole list is written out at once; the first and last run of a

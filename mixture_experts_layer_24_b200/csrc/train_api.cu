@@ -61,6 +61,45 @@ moe_status_t check_row_type(int dtype) {
   return MOE_OK;
 }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace of moe_route_bwd_topk: that of moe_route_bwd, the list of pairs, and the sort's scratch.
+struct SortedPairs {
+  size_t rank, chunk_counts, counts, offsets, perm_src, perm_k, inv, total;
+};
+
+SortedPairs sorted_pairs(size_t first, const moe_config_t& c, int T) {
+  const size_t pairs = (size_t)T * c.top_k * 4, experts = (size_t)c.n_experts * 4;
+  SortedPairs s{};
+  size_t o = align256(first);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  s.rank = take(pairs);
+  s.chunk_counts = take(64 * experts);  // permute_chunk_tokens makes at most 64 chunks
+  s.counts = take(experts);
+  s.offsets = take(experts + 4);
+  s.perm_src = take(pairs);
+  s.perm_k = take(pairs);
+  s.inv = take(pairs);
+  s.total = o;
+  return s;
+}
+
+moe_status_t check_route_bwd(const moe_ctx_t* ctx, const void* x, const float* topk_w, const float* dtopk_w, int T,
+                             const float* dlogit, const float* dw_router, const void* ws, size_t ws_bytes,
+                             size_t need) {
+  if (!dw_router) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  if (T > 0 && (!x || !topk_w || !dtopk_w || !dlogit)) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  if (!aligned16({x, dw_router})) return fail(MOE_ERR_INVALID_ARG, "x and dw_router must be 16-byte aligned");
+  if (need && (!ws || ws_bytes < need))
+    return fail(MOE_ERR_INVALID_ARG, "workspace too small (see moe_route_bwd_workspace_size)");
+  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return MOE_OK;
+}
+
 moe_status_t check_features(int n_in, int n_out) {
   if (n_in <= 0 || n_out <= 0) return fail(MOE_ERR_INVALID_ARG, "n_in and n_out must be positive");
   if (n_in % 128 || n_out % 128 || n_in > kMaxFeatures || n_out > kMaxFeatures)
@@ -218,14 +257,10 @@ moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales,
                            size_t ws_bytes, moe_stream_t stream) {
   moe_status_t st = check_tokens(ctx, T);
   if (st != MOE_OK) return st;
-  if (!offsets || !dw_router) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
-  if (T > 0 && (!x || !topk_w || !dtopk_w || !perm_src || !perm_k || !dlogit))
-    return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
-  if (!aligned16({x, dw_router})) return fail(MOE_ERR_INVALID_ARG, "x and dw_router must be 16-byte aligned");
-  const size_t need = moe_route_bwd_workspace_size(ctx, T);
-  if (need && (!ws || ws_bytes < need))
-    return fail(MOE_ERR_INVALID_ARG, "workspace too small (see moe_route_bwd_workspace_size)");
-  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (!offsets || (T > 0 && (!perm_src || !perm_k))) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  st = check_route_bwd(ctx, x, topk_w, dtopk_w, T, dlogit, dw_router, ws, ws_bytes,
+                       moe_route_bwd_workspace_size(ctx, T));
+  if (st != MOE_OK) return st;
   ON_DEVICE(ctx);
   const moe_config_t& c = ctx->cfg;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -234,6 +269,46 @@ moe_status_t moe_route_bwd(moe_ctx_t* ctx, const void* x, const float* x_scales,
   MOE_CUDA(launch_route_bwd(x, x_scales, topk_w, dtopk_w, offsets, perm_src, perm_k, T, c.top_k, c.n_experts, c.hidden,
                             dlogit, dw_router, dlogit_bias, static_cast<float*>(ws), ctx->d_status, s, ctx->chain));
   return MOE_OK;
+}
+
+size_t moe_route_bwd_topk_workspace_size(const moe_ctx_t* ctx, int T) {
+  if (!ctx || T < 0 || T > 65536) return 0;
+  return sorted_pairs(moe_route_bwd_workspace_size(ctx, T), ctx->cfg, T).total;
+}
+
+moe_status_t moe_route_bwd_topk(moe_ctx_t* ctx, const void* x, const float* x_scales, const int32_t* topk_idx,
+                                const float* topk_w, const float* dtopk_w, int T, float* dlogit, float* dw_router,
+                                float* dlogit_bias, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = check_tokens(ctx, T);
+  if (st != MOE_OK) return st;
+  if (T > 0 && !topk_idx) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  st = check_route_bwd(ctx, x, topk_w, dtopk_w, T, dlogit, dw_router, ws, ws_bytes,
+                       moe_route_bwd_topk_workspace_size(ctx, T));
+  if (st != MOE_OK) return st;
+  ON_DEVICE(ctx);
+  const moe_config_t& c = ctx->cfg;
+  const size_t own = moe_route_bwd_workspace_size(ctx, T);
+  const SortedPairs w = sorted_pairs(own, c, T);
+  auto at = [&](size_t o) { return reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + o); };
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int chunk = permute_chunk_tokens(T, c.top_k), n_chunks = (T + chunk - 1) / chunk;
+  if (T > 0) {
+    Prof p(ctx, MOE_PROF_PERMUTE, s);
+    MOE_CUDA(launch_permute_rank(topk_idx, T, c.top_k, c.n_experts, chunk, at(w.rank), at(w.chunk_counts),
+                                 ctx->d_status, s, false));
+  }
+  {
+    Prof p(ctx, MOE_PROF_PERMUTE, s);
+    MOE_CUDA(launch_permute_scan(at(w.chunk_counts), n_chunks, c.n_experts, at(w.counts), at(w.offsets), s,
+                                 ctx->chain && T > 0));
+  }
+  if (T > 0) {
+    Prof p(ctx, MOE_PROF_PERMUTE, s);
+    MOE_CUDA(launch_permute_scatter(topk_idx, at(w.rank), at(w.chunk_counts), at(w.offsets), T, c.top_k, c.n_experts,
+                                    chunk, at(w.perm_src), at(w.perm_k), at(w.inv), s, ctx->chain));
+  }
+  return moe_route_bwd(ctx, x, x_scales, topk_w, dtopk_w, at(w.offsets), at(w.perm_src), at(w.perm_k), T, dlogit,
+                       dw_router, dlogit_bias, ws, own, stream);
 }
 
 moe_status_t moe_expert_product(moe_ctx_t* ctx, const void* a, const void* w, const int32_t* offsets, int P, int n_in,

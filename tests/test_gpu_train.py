@@ -315,6 +315,98 @@ def test_route_bwd(layers, T, K, E, H, drop, ckpt):
     assert all(torch.equal(a, b) for a, b in zip((dl, dwr, db), again))
 
 
+@pytest.mark.parametrize("T,K,E,H,drop", [(1, 8, 384, 4096, 0.5), (9, 3, 8, 256, 0.3), (37, 8, 384, 256, 0.9),
+                                          (300, 2, 5, 2176, 0.2), (65, 32, 40, 384, 0.1), (1025, 8, 64, 1024, 0.05),
+                                          (600, 4, 1024, 128, 0.0), (64, 4, 16, 512, 1.0)])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_router_gradient_with_dropped_pairs_against_autograd(layers, T, K, E, H, drop, ckpt):
+    """dx (router and rows together), dw_router and dlogit_bias belong to one loss, whatever pairs the forward
+    dropped. w is rounded to fp32 and the reference's softmax sums to 1 in 64 bits: they are 2^-24 apart at most, twice
+    in a dlogit."""
+    import mixture_experts_layer_24_b200 as M
+    L, r = layers(H, E, K), _cuda(R.routing(T, K, E, 19, drop, T // 2 if drop else None))
+    x, rows = _rand(120, T, H), _poison_behind(_rand(121, T * K, H), r["n"])
+    wr, c = _rand(122, E, H, std=0.05, dtype=F32), _rand(123, T, K, dtype=F32)
+    scales, values = None, x
+    if ckpt:
+        codes = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+        scales = torch.empty((T, H // 128), device="cuda")
+        M.moe_quantize_e4m3(x, T, H, 1, codes, scales)
+        values, x = R.decode(codes, scales), codes
+    # the weights' gradient comes from the combine, so that of dropped pairs is its 0
+    dw = torch.where(r["inv"] >= 0, c, torch.zeros_like(c))
+    dl, dwr, db = L.route_bwd(x, r["w"], dw, x_scales=scales, topk_idx=r["idx"])
+    dx = L.dispatch_bwd(rows, r["inv"], dl, r["idx"], wr)
+    dx_ref, dwr_ref, db_ref = R.route_bwd_by_autograd(values, wr, r["w"], dw, r["idx"], rows, r["inv"])
+    everyone = torch.zeros_like(r["inv"])
+    _, _, _, dl_mag, dwr_mag, db_mag = R.route_bwd(values, r["w"], dw, r["idx"], everyone, E)
+    most = int(torch.bincount(r["idx"].view(-1).long()).max())
+    _within(dwr, dwr_ref, (K + 6 + most) * U * dwr_mag * 1.01, "dw_router")
+    _within(db, db_ref, (K + 5 + most) * U * db_mag * 1.01, "dlogit_bias")
+    _, mag = R.dispatch_bwd(rows, r["inv"], dl_mag, r["idx"], wr.abs())
+    _within(dx, dx_ref, (3 * K + 4) * U * mag * 1.01 + R.BF16_HALF * dx_ref.abs() * 1.01, "dx")
+    assert L.status() == 0
+    again = L.route_bwd(x, r["w"], dw, x_scales=scales, topk_idx=r["idx"])
+    assert all(torch.equal(a, b) for a, b in zip((dl, dwr, db), again))
+    # the list of every chosen pair gives the same bits
+    _, offsets, perm_src, perm_k, _ = L.permute(r["idx"])
+    listed = L.route_bwd(x, r["w"], dw, offsets, perm_src, perm_k, x_scales=scales)
+    assert all(torch.equal(a, b) for a, b in zip((dl, dwr, db), listed))
+
+
+def test_router_gradient_of_the_choice_refusals_and_marks(layers):
+    """Refused on the host before any launch; an index that names no expert adds nothing and is reported; no tokens;
+    a captured call, replayed on new inputs; another stream."""
+    import mixture_experts_layer_24_b200 as M
+    T, K, E, H = 6, 2, 8, 256
+    L, r = layers(H, E, K), _cuda(R.routing(T, K, E, 30))
+    x, dw = _rand(131, T, H), _rand(132, T, K, dtype=F32)
+    need = M.moe_route_bwd_topk_workspace_size(L.ctx, T)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dl, dwr, db = torch.empty_like(dw), torch.empty((E, H), device="cuda"), torch.empty(E, device="cuda")
+    c, w, idx, before = L.ctx, r["w"], r["idx"], L.launches()
+    calls = [
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, None, w, dw, T, dl, dwr, db, ws)),
+        (1, lambda: M.moe_route_bwd_topk(c, None, None, idx, w, dw, T, dl, dwr, db, ws)),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, None, T, dl, dwr, db, ws)),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, T, None, dwr, db, ws)),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, T, dl, None, db, ws)),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, T, dl, dwr, db, None)),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, T, dl, dwr, db, ws[:-1])),
+        (1, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, -1, dl, dwr, db, ws)),
+        (2, lambda: M.moe_route_bwd_topk(c, x, None, idx, w, dw, 65537, dl, dwr, db, ws)),
+    ]
+    for i, (status, call) in enumerate(calls):
+        with pytest.raises(M.MoeError) as e:
+            call()
+        assert e.value.status == status, (i, e.value)
+    assert L.launches() == before and L.status() == 0
+    assert M.moe_route_bwd_topk_workspace_size(c, -1) == 0 and M.moe_route_bwd_topk_workspace_size(c, 65537) == 0
+    marked = idx.clone()
+    marked[2, 1], marked[4, 0] = E, -1
+    _, off, src, pk, _ = L.permute(marked)
+    want = L.route_bwd(x, w, dw, off, src, pk)
+    assert L.status() == M.binding.MOE_DEV_BAD_EXPERT
+    got = L.route_bwd(x, w, dw, topk_idx=marked)
+    assert L.status() == M.binding.MOE_DEV_BAD_EXPERT and all(torch.equal(a, b) for a, b in zip(got, want))
+    none = torch.empty((0, K), dtype=torch.int32, device="cuda")
+    empty = L.route_bwd(x[:0], w[:0], dw[:0], topk_idx=none)
+    assert empty[0].shape == (0, K) and (empty[1] == 0).all() and (empty[2] == 0).all()
+    xin = x.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = L.route_bwd(xin, w, dw, topk_idx=idx)
+    xin.copy_(_rand(133, T, H))
+    g.replay()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = L.route_bwd(xin, w, dw, topk_idx=idx, stream=side)
+    torch.cuda.synchronize()
+    want = L.route_bwd(_rand(133, T, H), w, dw, topk_idx=idx)
+    assert all(torch.equal(a, b) and torch.equal(o, b) for a, o, b in zip(out, other, want)) and L.status() == 0
+
+
 def _segments(counts, slack=0):
     off = torch.zeros(len(counts) + 1, dtype=torch.int32)
     off[1:] = torch.cumsum(torch.tensor(counts), 0)

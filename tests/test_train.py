@@ -138,6 +138,34 @@ def test_layer_methods_refuse_bad_arguments_before_any_call(host_layer):
         assert not calls, f"bad call {i} reached the C ABI"
 
 
+def test_router_gradient_takes_the_choice_or_a_list_of_pairs(host_layer, monkeypatch):
+    from mixture_experts_layer_24_b200 import binding as B
+    L, calls = host_layer
+    monkeypatch.setattr(B, "moe_route_bwd_topk_workspace_size", lambda ctx, T: 64)
+    monkeypatch.setattr(B, "moe_route_bwd_topk", lambda *a, **k: calls.append("moe_route_bwd_topk"))
+    a = _args()
+    bad = [
+        lambda: L.route_bwd(a["x"], a["w"], a["w"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], a["offsets"], a["perm"], a["perm"], topk_idx=a["idx"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], perm_k=a["perm"], topk_idx=a["idx"]),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], topk_idx=a["idx"].long()),
+        lambda: L.route_bwd(a["x"], a["w"], a["w"], topk_idx=a["idx"][:-1]),
+        lambda: L.route_bwd(a["x"], a["w"][:, :1], a["w"], topk_idx=a["idx"]),
+    ]
+    for f in bad:
+        with pytest.raises((TypeError, ValueError)):
+            f()
+    assert not calls
+    dl, dwr, db = L.route_bwd(a["x"], a["w"], a["w"], topk_idx=a["idx"])
+    assert dl.shape == (5, 2) and dwr.shape == (8, 256) and db.shape == (8,) and calls == ["moe_route_bwd_topk"]
+
+
+def test_router_gradient_of_a_null_context_is_refused(lib):
+    N = None
+    assert lib.moe_route_bwd_topk_workspace_size(N, 4) == 0
+    assert lib.moe_route_bwd_topk(N, N, N, N, N, N, 1, N, N, N, N, 0, N) == 1
+
+
 def test_train_step_order_of_calls(host_layer):
     from mixture_experts_layer_24_b200 import train
     L, calls = host_layer
@@ -197,6 +225,28 @@ def test_gradient_formulas_against_differences():
         for i in at:
             d = _difference(loss, value, i)
             assert abs(d - grad.reshape(-1)[i].item()) <= 1e-6 * (1 + abs(d)), i
+
+
+def test_router_gradient_formula_with_dropped_pairs():
+    """The router's gradient sums over every chosen pair: with pairs and a whole token dropped, the formula over all
+    pairs is autograd's, and the formula over the kept ones is not."""
+    T, K, E, H = 9, 3, 7, 16
+    r = R.routing(T, K, E, seed=5, drop=0.3, drop_token=4)
+    g = torch.Generator().manual_seed(6)
+    x, wr, dw = (torch.randn(*s, generator=g, dtype=F64) for s in ((T, H), (E, H), (T, K)))
+    rows = torch.randn(T * K, H, generator=g, dtype=F64)
+    dx_ref, dwr_ref, db_ref = R.route_bwd_by_autograd(x, wr, r["w"], dw, r["idx"], rows, r["inv"])
+    kept = r["inv"] >= 0
+    assert 3 < int((~kept).sum()) < T * K
+    dw = torch.where(kept, dw, torch.zeros((), dtype=F64))
+    w = r["w"].to(F64) / r["w"].to(F64).sum(1, keepdim=True)
+    everyone = torch.zeros_like(r["inv"])  # no pair marked as dropped
+    dl, dwr, db = R.route_bwd(x, w, dw, r["idx"], everyone, E)[:3]
+    dx, _ = R.dispatch_bwd(rows, r["inv"], dl, r["idx"], wr)
+    for got, ref in ((dx, dx_ref), (dwr, dwr_ref), (db, db_ref)):
+        assert torch.allclose(got, ref, rtol=1e-12, atol=1e-12)
+    listed = R.route_bwd(x, w, dw, r["idx"], r["inv"], E)[1]
+    assert (listed - dwr_ref).norm() > 0.1 * dwr_ref.norm()
 
 
 def test_oracle_quantiser_is_the_checkpoint_rule():

@@ -98,6 +98,20 @@ def route_bwd(x, w, dw, idx, inv, E):
     return dl, full.t() @ x.to(F64), full.sum(0), mag, fmag.t() @ x.to(F64).abs(), fmag.sum(0)
 
 
+def route_bwd_by_autograd(x, wr, w, dw, idx, rows, inv):
+    """(dx, dWr, dbias) in float64, by autograd, of a loss that sees the routing weights and the kept rows:
+    sum over kept pairs of softmax(l)[t,k] * dw[t,k] + <x[t], rows[inv[t,k]]>, where l = x Wr^T + b over the K chosen
+    logits is shifted by constants so that softmax(l) is w. Dropped pairs are in the softmax and nowhere else."""
+    x, wr = x.to(F64).clone().requires_grad_(), wr.to(F64).clone().requires_grad_()
+    b = torch.zeros(wr.shape[0], dtype=F64, device=x.device, requires_grad=True)
+    kept = inv >= 0
+    upstream = torch.where(kept, dw.to(F64), torch.zeros((), dtype=F64, device=x.device))
+    logits = torch.gather(x @ wr.t() + b, 1, idx.long())
+    weights = torch.softmax(logits + (torch.log(w.to(F64)) - logits).detach(), 1)
+    ((weights * upstream).sum() + (x[:, None] * gathered(rows, inv)).sum()).backward()
+    return x.grad, wr.grad, b.grad
+
+
 def products(a, w, offsets, transposed):
     """(out, sum of |terms|) of the kept rows."""
     cut = offsets.tolist()
