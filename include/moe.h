@@ -443,7 +443,10 @@ moe_status_t moe_expert_product(moe_ctx_t* ctx, const void* a, const void* w, co
  * dw [E, n_out, n_in] bf16 or fp32 (dtype MOE_T_BF16 / MOE_T_F32), written
  * whole (zeros for experts without rows) or, with accumulate != 0 (fp32 only),
  * added to what is there (fp32 add; a subnormal sum becomes 0). dy [P, n_out], a [P, n_in] bf16; rows of other
- * experts and behind offsets[E] may hold anything. Limits as above. */
+ * experts and behind offsets[E] may hold anything. Limits as above.
+ * The tensor cores' fp32 sum cuts products off at its last place, so it is restarted every 896 rows (fp32 gradient:
+ * about 1e-6 of the terms' magnitudes off, at any number of rows) or 32768 rows (bf16 gradient: at most half a step of
+ * bf16 beside its rounding); the parts are added in fp32. */
 moe_status_t moe_expert_wgrad(moe_ctx_t* ctx, const void* dy, const void* a, const int32_t* offsets, int P, int n_in,
                               int n_out, int dtype, int accumulate, void* dw, moe_stream_t stream);
 

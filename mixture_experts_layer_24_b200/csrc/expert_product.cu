@@ -24,11 +24,15 @@
 // gradient, both operands of the weights' gradient) the box is MN-major and
 // the MMA reads it transposed, so nothing is ever transposed in memory.
 //
-// An fp32 weights' gradient is summed in segments of K (kSegment), the first
-// one stored, the others added by the TMA in L2, by the same thread one after
-// the other: the tensor cores' own running sum drifts over thousands of steps.
-// A bf16 gradient is one run (its rounding, 2^-9, is larger up to a million
-// rows), and so are the other two forms (K at most 16384).
+// The tensor cores align each product to the running sum and cut it off there,
+// so a long run drifts towards zero: up to 2^-23 of the running sum per row in
+// the worst case (5e-9 to 1e-8 of the sum per row for positive terms, measured).
+// An fp32 weights' gradient is therefore summed in segments of K (kSegment),
+// the first one stored, the others added by the TMA in L2, by the same thread
+// one after the other. A bf16 gradient is summed in runs of kLongRun, which are
+// added up in fp32 in TMEM and rounded once: 2^15 rows cannot drift further
+// than half a step of bf16 (2^-8). The other two forms are one run (K at most
+// 2^14).
 //
 // In the weights' gradient K is the expert's own rows. Whole groups of 16 rows
 // (one MMA's K) go through the stages; groups that reach into the next expert's
@@ -83,11 +87,16 @@ constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 12
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
 __host__ __device__ constexpr int barriers(bool wgrad) { return 2 * stages(wgrad) + 10; }
-// K steps summed in TMEM before an fp32 gradient goes out. The tensor cores' running sum loses about 1.4e-9 of itself
-// per row: a gradient over 16384 rows summed in one run was 1.9e-5 off (2-norm), over 65536 rows 7.6e-5. In segments of
-// 14 steps (896 rows) it stays under 1e-6 for any number of rows. Time at 8192 rows, 4096 x 4096: 238 us in one run,
-// 252 us in segments of 32 steps, 272 us of 16, 286 us of 14, 326 us of 8.
+// K steps summed in TMEM before an fp32 gradient goes out. Over 16384 rows in one run it was 1.9e-5 off (2-norm, terms of
+// both signs), over 65536 rows 7.6e-5. In segments of 14 steps (896 rows) the error does not grow with the rows: 6.5e-7
+// (terms of both signs), or 1.5e-6 low (positive terms), where fp32 multiply-adds have 1.9e-7. Time at 8192 rows,
+// 4096 x 4096: 238 us in one run, 252 us in segments of 32 steps, 272 us of 16, 286 us of 14, 326 us of 8.
 constexpr int kSegment = 14;
+// K steps of one run of a bf16 gradient (32768 rows). Without it, positive terms over 65536 rows came out 6.5e-4 low,
+// over 524288 rows 3.2e-3, over 2097152 rows 1.2e-2. The sum of the runs so far stays in one accumulator while the
+// other takes the next run; the MMA waits while the epilogue adds it (one expert of 131072 rows, 4096 x 4096: within the
+// noise of one run's time). Experts of up to 32768 rows are summed as before it.
+constexpr int kLongRun = 512;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
 constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes
 constexpr uint32_t kPieceBytes = 32 * 256;        // 32 rows x 128 features
@@ -208,6 +217,19 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -246,6 +268,16 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+
+// The two TMEM accumulators as the MMA warp and the epilogue walk them, in step. A tile takes them in turn, one per
+// segment, except where it carries its sum: then the first segment's holds the sum and the others all use the other.
+struct Accumulators {
+  int next = 0;
+  uint32_t phases = 0;  // bit b: parity of the uses of accumulator b
+  __device__ int of(int seg, bool carry) const { return carry && seg > 0 ? next ^ 1 : next; }
+  __device__ uint32_t phase(int b) const { return (phases >> b) & 1u; }
+  __device__ void used(int b) { phases ^= 1u << b; }
+};
 
 struct Tile {
   int e, m0, row0, rows, n0, n;  // n0, n: first column and width of the N axis (weights' gradient: input features)
@@ -393,7 +425,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
   // An fp32 gradient over many rows is summed in segments of at most kSegment K steps: the first is stored, the others
   // are added in L2.
-  auto segments = [&](int KB) { return kWG && a.out_f32 && KB > kSegment ? (KB + kSegment - 1) / kSegment : 1; };
+  // A bf16 one carries its sum from one long run to the next.
+  auto segments = [&](int KB) {
+    const int longest = a.out_f32 ? kSegment : kLongRun;
+    return kWG && KB > longest ? (KB + longest - 1) / longest : 1;
+  };
+  auto carries = [&](int nseg) { return kWG && !a.out_f32 && nseg > 1; };
   auto k_steps = [&](const Tile& t) { return kWG ? (t.rows + 48) / 64 : a.k_total / 64; };  // steps with a whole group
   auto tail_rows = [&](const Tile& t) { return kWG ? t.rows & 15 : 0; };
 
@@ -468,7 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // The whole warp walks the steps and one lane issues: warp-uniform code keeps descriptors in uniform registers,
     // without a move to them before each MMA.
     if (rank == 0) {
-      int consumed = 0, j = 0, n_tails = 0;
+      int consumed = 0, n_tails = 0;
+      Accumulators acc;
       const int n_all = uniform(total);
       Rows raw = ahead(cluster);
       for (int tile = cluster; tile < n_all; tile += n_clusters) {
@@ -479,10 +517,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int KB = uniform(k_steps(t)), nseg = uniform(segments(KB)), tail = uniform(tail_rows(t));
         const uint32_t idesc =
             instr_desc(256, uniform(t.n), 1u) | (kMmn ? 1u << 15 : 0u) | (kNmn ? 1u << 16 : 0u);
+        const bool carry = carries(nseg);
         bool ok = true;
-        for (int seg = 0; ok && seg < nseg; ++seg, ++j) {
-          const int buf = j & 1;
-          ok = j < 2 || __all_sync(0xffffffffu, mbar_wait(tempty(buf), ((j >> 1) - 1) & 1));
+        for (int seg = 0; ok && seg < nseg; ++seg) {
+          const int buf = acc.of(seg, carry);
+          ok = __all_sync(0xffffffffu, mbar_wait(tempty(buf), acc.phase(buf) ^ 1u));  // passes before the first use
+          acc.used(buf);
+          if (!carry || seg == nseg - 1) acc.next ^= 1;
           tc_fence_after();
           const uint32_t d = tmem_u + buf * kTileN;
           const int kb0 = KB * seg / nseg, kb1 = KB * (seg + 1) / nseg;
@@ -570,7 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    int j = 0, piece = 0;  // piece: staged pieces so far
+    Accumulators acc;
+    int piece = 0;  // staged pieces so far
     bool gave_up = false;
     Rows raw = ahead(cluster);
     for (int tile = cluster; tile < total && !gave_up; tile += n_clusters) {
@@ -580,10 +622,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!any && a.accumulate) continue;  // nothing to add
       const bool in_m = t.m0 + (int)rank * 128 < a.m_total;  // CTA-uniform
       const int nseg = segments(k_steps(t));
+      const bool carry = carries(nseg);
+      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
       for (int seg = 0; seg < nseg && !gave_up; ++seg) {
-        const int buf = j & 1;
+        const int buf = acc.of(seg, carry);
+        const uint32_t tl = tmem + buf * kTileN + lanes, held = tmem + (buf ^ 1) * kTileN + lanes;  // held: with carry
         if (any) {
-          if (lane == 0 && !mbar_wait(tfull(buf), (j >> 1) & 1)) *ep_abort = 1;
+          if (lane == 0 && !mbar_wait(tfull(buf), acc.phase(buf))) *ep_abort = 1;
           named_bar_sync(2, 128);  // the four warps leave the loop together or not at all
           if (*ep_abort) {
             if (lane == 0) {
@@ -594,12 +639,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
+          acc.used(buf);
+          if (!carry || seg == nseg - 1) acc.next ^= 1;
         }
-        const bool add = kWG && (a.accumulate || seg > 0);
+        if (carry && seg < nseg - 1) {  // this run joins the sum of those before it
+          if (seg == 0) continue;
+          if (in_m) {
+#pragma unroll 1
+            for (int c = 0; c < t.n; c += 32) {
+              uint32_t v[32], sum[32];
+              tmem_ld32(tl + c, v);
+              tmem_ld32(held + c, sum);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                sum[q] = __float_as_uint(__uint_as_float(sum[q]) + __uint_as_float(v[q]));
+              tmem_st32(held + c, sum);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
+          continue;
+        }
+        const bool joins = kWG && seg > 0 && !carry;  // adds to the segments stored before it
+        const bool add = joins || (kWG && a.accumulate);
         // what this warp stored of the last segment is in place before it adds to it
-        if (kWG && seg > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (joins && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (in_m) {
-          const uint32_t tl = tmem + buf * kTileN + (static_cast<uint32_t>(warp * 32) << 16);
           const int cols = kWG ? t.n : t.rows;
           // columns per step: a 128-byte store box of the output type, or 32 rows of the output
           const int step = kWG && !a.out_f32 ? 64 : 32;
@@ -610,6 +677,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (any) {
                 tmem_ld32(tl + at, v);
                 tmem_wait_ld();
+                if (carry) {  // the last run and the sum of the others
+                  uint32_t sum[32];
+                  tmem_ld32(held + at, sum);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int q = 0; q < 32; ++q)
+                    v[q] = __float_as_uint(__uint_as_float(sum[q]) + __uint_as_float(v[q]));
+                }
               } else {
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = 0u;
@@ -672,8 +747,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (any) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) remote_arrive(map_rank(tempty(buf), 0));
-          ++j;
+          if (lane == 0) {
+            remote_arrive(map_rank(tempty(buf), 0));
+            if (carry) remote_arrive(map_rank(tempty(buf ^ 1), 0));
+          }
         }
       }
     }

@@ -513,6 +513,43 @@ def test_wgrad_fp32_over_many_rows(layers):
     _within(half, ref, (1024 * 2.0 ** -23 + R.BF16_HALF) * mag * 1.01, "bf16 dw")
 
 
+def test_wgrad_bf16_over_the_most_rows(layers):
+    """Positive terms over every number of rows accepted up to the most, where nothing cancels what the tensor cores'
+    sum cuts off: a run of 2^15 rows loses at most one unit (2^-23) of its sum per row, 2^-8 in all; the runs (64 at
+    most) are added in fp32, and the sum is rounded once to bf16."""
+    L = layers(256, 1, 1, 128)
+    for P in (32768, 65536, 300001, 65536 * 32):
+        off = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+        a, dy = _rand(140, P, 128).abs_(), _rand(141, P, 128).abs_()
+        ref = torch.zeros((128, 128), dtype=F64, device="cuda")
+        for i in range(0, P, 65536):
+            ref += dy[i:i + 65536].to(F64).t() @ a[i:i + 65536].to(F64)
+        got = L.expert_wgrad(dy, a, off)[0]
+        _within(got, ref, (2.0 ** -8 + 64 * U + R.BF16_HALF) * ref * 1.01, f"bf16 dw over {P} rows")
+        # no bias beyond a quarter of the rounding's half step: over 16384 elements the roundings average out
+        assert abs(((got.to(F64) - ref) / ref).mean()) <= R.BF16_HALF / 4, P
+        assert torch.equal(got, L.expert_wgrad(dy, a, off)[0])
+    assert L.status() == 0
+
+
+def test_wgrad_bf16_runs_of_whole_numbers(layers):
+    """Experts of one run, of several, with and without a ragged end, none and few rows, in many tiles per CTA pair:
+    sums of whole numbers are exact in fp32 and rounded once, so every bit is pinned."""
+    counts = [40000, 5, 70001, 0, 32768, 32769, 32784, 65552, 16, 98320, 1]
+    L, (off, P) = layers(256, len(counts), 1, 128), _segments(counts, 7)
+    n = P - 7
+    for n_in, n_out in ((1280, 1024), (128, 384)):
+        a, dy = _ints(142, P, n_in), _ints(143, P, n_out)
+        _poison_behind(a, n)
+        _poison_behind(dy, n)
+        got = L.expert_wgrad(dy, a, off)
+        cut = off.tolist()
+        for e, (i, j) in enumerate(zip(cut, cut[1:])):
+            ref = dy[i:j].to(F64).t() @ a[i:j].to(F64)
+            assert torch.equal(got[e], ref.to(F32).to(BF16)), counts[e]
+    assert L.status() == 0
+
+
 def test_wgrad_without_any_row(layers):
     L = layers(256, 3, 1, 128)
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
