@@ -191,7 +191,7 @@ moe_status_t encode_2d(moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, bool fp8
   const cuuint64_t strides[1] = {inner * (fp8 ? 1 : 2)};
   const cuuint32_t box[2] = {fp8 ? 128u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = ctx->encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  const CUresult r = ctx->encode_tiled(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -207,7 +207,7 @@ moe_status_t encode_3d_bf16(moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uin
   const cuuint64_t strides[2] = {inner * 2, 128};
   const cuuint32_t box[3] = {64u, box_rows, kc};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = ctx->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+  const CUresult r = ctx->encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
                                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed: " + std::to_string((int)r));
@@ -223,7 +223,7 @@ moe_status_t encode_3d_fp4(moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uint
   const cuuint64_t strides[2] = {inner / 2, 64};
   const cuuint32_t box[3] = {128u, 128u, (cuuint32_t)kMxKC};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = ctx->encode(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides,
+  const CUresult r = ctx->encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides,
                                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (E2M1) failed: " + std::to_string((int)r));
@@ -239,7 +239,7 @@ moe_status_t encode_3d_u8(moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uint6
   const cuuint64_t strides[2] = {inner, 128};
   const cuuint32_t box[3] = {128u, box_rows, (cuuint32_t)kMxKC};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = ctx->encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
+  const CUresult r = ctx->encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
                                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (3-D bytes) failed: " + std::to_string((int)r));

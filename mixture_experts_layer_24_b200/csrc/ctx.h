@@ -47,6 +47,18 @@ struct moe_ctx {
   int64_t prof_n[MOE_PROF_KINDS] = {};
   std::mutex prof_mu;
 
+  // cuTensorMapEncodeTiled on the current device. It is a driver call and needs that device's context current on this
+  // thread; a thread whose first CUDA call this is has none yet (cudaGetDevice binds nothing, cudaSetDevice does).
+  template <typename... Args>
+  CUresult encode_tiled(Args... args) const {
+    CUresult r = encode(args...);
+    int current = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&current) == cudaSuccess &&
+        cudaSetDevice(current) == cudaSuccess)
+      r = encode(args...);
+    return r;
+  }
+
   cudaEvent_t take_event() {
     if (!ev_pool.empty()) {
       cudaEvent_t e = ev_pool.back();

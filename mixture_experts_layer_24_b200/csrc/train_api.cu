@@ -114,7 +114,7 @@ moe_status_t encode(const moe_ctx_t* ctx, CUtensorMap* m, const void* ptr, uint6
   const cuuint64_t strides[1] = {inner * (f32 ? 4 : 2)};
   const cuuint32_t box[2] = {f32 ? 32u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = ctx->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  const CUresult r = ctx->encode_tiled(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

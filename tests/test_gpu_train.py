@@ -828,6 +828,52 @@ def test_calls_from_two_threads(layers):
     assert L.status() == 0
 
 
+def _in_a_new_thread(f):
+    import threading
+    result = []
+
+    def run():
+        try:
+            result.append((f(), None))
+        except Exception as e:  # surfaced below
+            result.append((None, e))
+
+    th = threading.Thread(target=run)
+    th.start()
+    th.join(timeout=120)
+    value, error = result[0]
+    if error is not None:
+        raise error
+    return value
+
+
+def test_first_call_of_a_thread(layers):
+    """A call whose thread has made no CUDA call before (outputs at hand, so not even an allocation): the products,
+    whose tensor maps come from the driver, and the registration of experts."""
+    import mixture_experts_layer_24_b200 as M
+    T, K, E, H, I = 9, 2, 8, 256, 128
+    L, r = M.MoeLayer(H, E, K, I), _cuda(R.routing(T, K, E, 150))
+    w_gu, w_dn = _rand(151, E, 2 * I, H, std=0.1), _rand(152, E, H, I, std=0.1)
+    a, x = _rand(153, T * K, H), _rand(154, T, H)
+    want = L.expert_product(a, w_gu, r["offsets"])
+    dw = L.expert_wgrad(want, a, r["offsets"])
+    out, dw2 = torch.zeros_like(want), torch.zeros_like(dw)
+    torch.cuda.synchronize()
+    _in_a_new_thread(lambda: L.expert_product(a, w_gu, r["offsets"], out=out))
+    _in_a_new_thread(lambda: L.expert_wgrad(want, a, r["offsets"], out=dw2))
+    for e in range(E):
+        _in_a_new_thread(lambda: L.register(e, w_gu[e], w_dn[e]))
+    y = torch.zeros((T * K, H), dtype=F32, device="cuda")
+    ws = L.workspace(T)
+    torch.cuda.synchronize()
+    _in_a_new_thread(lambda: M.moe_expert_ffn(L.ctx, L.slots, x, r["perm_src"], r["perm_k"], r["offsets"], r["w"], T,
+                                              y, ws))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(dw2, dw)
+    assert torch.equal(y, L.expert_ffn(x, r["perm_src"], r["perm_k"], r["offsets"], r["w"])) and L.status() == 0
+    L.close()
+
+
 def test_launches_are_counted_and_timed(layers):
     """moe_launch_count and moe_profile_* see the training calls under their own kinds."""
     import mixture_experts_layer_24_b200 as M
