@@ -774,8 +774,11 @@ cudaError_t launch_form(const ProductMaps& maps, const ProductArgs& a, long long
   // 226 KB at most (a CTA may have 227)
   const size_t smem = 1024 + (size_t)stages(kWG) * kStageBytes + staging_bytes(kWG) + (kWG ? 2 * kTailBytes : 0) +
                       8 * barriers(kWG) + 16 + (kWG ? 0 : 4 * (3 * (size_t)a.E + 1));
+  // The limit belongs to the kernel, not to the call: one by this call's E could be lowered by another thread, for a
+  // layer of fewer experts, before the launch below.
+  constexpr int kMostSmem = 227 * 1024;
   const cudaError_t err = cudaFuncSetAttribute(expert_product_kernel<FORM>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (err != cudaSuccess) return err;
   const long long clusters = std::max(1LL, std::min<long long>(num_sms / 2, max_tiles));
   expert_product_kernel<FORM><<<dim3((unsigned)(2 * clusters)), dim3(kThreads), smem, s>>>(maps, a);

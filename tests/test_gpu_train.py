@@ -828,6 +828,50 @@ def test_calls_from_two_threads(layers):
     assert L.status() == 0
 
 
+def _hammer(calls, rounds):
+    """Each call from a thread and on a stream of its own, many times over, straight through the C function (which lets
+    go of the interpreter's lock). Returns the errors."""
+    import threading
+    import mixture_experts_layer_24_b200 as M
+    errors = []
+
+    def run(call):
+        stream = torch.cuda.Stream()
+        for i in range(rounds):
+            if call(stream.cuda_stream) != 0:
+                errors.append(M.lib().moe_last_error().decode())
+            if i % 100 == 0:
+                stream.synchronize()
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(c,)) for c in calls]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(timeout=240)
+    assert not any(th.is_alive() for th in threads)
+    return errors
+
+
+def test_products_of_two_layers_from_two_threads(layers):
+    """Layers of 8 and of 1024 experts, whose launches need different amounts of shared memory."""
+    import mixture_experts_layer_24_b200 as M
+    calls, kept = [], []
+    for E in (8, 1024, 8, 1024):
+        L, (off, P) = layers(256, E, 1, 128), _segments([0] * (E - 1) + [3])
+        for transposed in (0, 1):
+            a, w = _ints(155 + E, P, 128), _ints(156 + E, E, 128, 128)
+            out = torch.zeros_like(a)
+            args = (L.ctx, a.data_ptr(), w.data_ptr(), off.data_ptr(), P, 128, 128, transposed, out.data_ptr())
+            calls.append(lambda s, args=args: M.lib().moe_expert_product(*args, s))
+            kept.append((L, a, w, off, out, transposed))
+    torch.cuda.synchronize()
+    errors = _hammer(calls, 4000)
+    assert not errors, (len(errors), errors[0])
+    for L, a, w, off, out, transposed in kept:
+        assert torch.equal(out, L.expert_product(a, w, off, transposed=bool(transposed))) and L.status() == 0
+
+
 def _in_a_new_thread(f):
     import threading
     result = []
