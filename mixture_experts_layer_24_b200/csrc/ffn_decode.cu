@@ -494,9 +494,12 @@ static cudaError_t launch_decode(const CUtensorMap& xmap, const ActMaps& hmaps, 
                                  const DecodeArgs& d, int grid, cudaStream_t s, bool pdl) {
   using C = DecodeCfg<TP>;
   const size_t smem = C::smem(d.E);
-  if (smem > 232448) return cudaErrorInvalidValue;
+  // The limit belongs to the kernel, not to the call: one by this call's E could be lowered by another thread, for a
+  // layer of fewer experts, before the launch below.
+  constexpr int kMostSmem = 227 * 1024;
+  if (smem > kMostSmem) return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(ffn_bf16_decode_kernel<TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+                                         kMostSmem);
   if (err != cudaSuccess) return err;
   const int persistent = grid < a.num_sms ? grid : a.num_sms;
   if (persistent <= 0) return cudaSuccess;

@@ -945,7 +945,8 @@ static cudaError_t launch_fp8(const ActMaps& maps, GemmArgs a, int grid, cudaStr
   a.stages = C::stages(KB);
   const size_t smem = C::smem(KB);
   auto kern = ffn_fp8_kernel<MODE, BN>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The most a CTA may have, not this call's smem: another thread could lower that limit before the launch below.
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (err != cudaSuccess) return err;
   const int persistent = grid < a.num_sms ? grid : a.num_sms;  // one CTA per SM walks the tiles
   if (persistent <= 0) return cudaSuccess;

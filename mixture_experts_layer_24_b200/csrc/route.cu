@@ -388,6 +388,7 @@ cudaError_t launch_route_gemm(const void* x, const float* wr, const float* bias,
 // the group's top-k, one warp per token, and returns the counter to zero;
 // otherwise a top-k kernel follows.
 constexpr int kRsWarps = 4;
+constexpr int kRsMostSmem = 200 * 1024;  // of a launch; larger H takes the kernels without staging
 
 __host__ __device__ constexpr size_t route_small_smem(int tg, int H) {
   return 16 + (size_t)kRsWarps * H * 4 + (size_t)tg * H * 2;
@@ -485,8 +486,9 @@ static cudaError_t launch_rs(const void* x, const float* wr, const float* bias, 
                              cudaStream_t s, int* sched, int sched_n, const ResidencyDev* rd = nullptr,
                              int32_t* map_of = nullptr) {
   const size_t smem = route_small_smem(TG, H);
+  // One limit for every call: another thread could lower that of this call's H before the launch below.
   cudaError_t err = cudaFuncSetAttribute(route_small_kernel<TG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+                                         kRsMostSmem);
   if (err != cudaSuccess) return err;
   dim3 grid((E + kRsWarps - 1) / kRsWarps, (T + TG - 1) / TG);
   return launch_ex(route_small_kernel<TG>, grid, dim3(kRsWarps * 32), smem, s, false,
@@ -508,7 +510,7 @@ cudaError_t launch_route_small(const void* x, const float* wr, const float* bias
   if (planned) *planned = false;
   if (T <= 0) return cudaSuccess;
   const bool bulk_ok = ((uintptr_t)x % 16 == 0) && ((uintptr_t)wr % 16 == 0) && (H % 8 == 0) &&
-                       route_small_smem(8, H) <= 200 * 1024;
+                       route_small_smem(8, H) <= kRsMostSmem;
   if (!bulk_ok) {
     if (sched) cudaMemsetAsync(sched, 0, sizeof(int) * sched_n, s);
     cudaError_t err = launch_router_logits(x, wr, bias, T, H, E, logits, s);
