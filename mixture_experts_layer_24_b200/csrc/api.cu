@@ -37,7 +37,7 @@ namespace {
 thread_local std::string g_last_error;
 
 moe_status_t fail(moe_status_t st, const std::string& msg) {
-  g_last_error = msg;
+  record_error(msg.c_str());
   return st;
 }
 
@@ -45,7 +45,12 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-void moe::record_error(const char* msg) { g_last_error = msg ? msg : ""; }
+// Every refusal and failure ends here. What the runtime remembers of it goes with it (the library has a runtime of its
+// own): a later launch that asks cudaGetLastError would take an allocation refused long before for its own failure.
+void moe::record_error(const char* msg) {
+  g_last_error = msg ? msg : "";
+  cudaGetLastError();
+}
 
 struct moe_slots {
   moe_ctx* ctx = nullptr;

@@ -229,3 +229,49 @@ def test_failed_mxfp4_scale_allocation_then_registration_works():
         assert layer.status() == 0
         layer.close()
     assert np.array_equal(outs[0], outs[1])
+
+
+def test_a_refused_allocation_is_reported_once():
+    """The device refuses one allocation larger than its memory (402 GB of spare slots): that call says so, and no later
+    call of any layer reports it again."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import mixture_experts_layer_24_b200 as M
+    T, H, E, K, I = 6, 256, 8, 2, 128
+    L = M.MoeLayer(H, E, K, I)
+    bf, dev = torch.bfloat16, "cuda"
+    x, wr = torch.randn(T, H, device=dev).to(bf), torch.randn(E, H, device=dev)
+    idx, w = L.route(x, wr)
+    _, offsets, perm_src, perm_k, inv = L.permute(idx)
+    rows, gu, dh = (torch.randn(T * K, n, device=dev).to(bf) for n in (H, 2 * I, I))
+    w_gu = torch.randn(E, 2 * I, H, device=dev).to(bf)
+    h, q, s = L.swiglu_ckpt(gu, inv)
+    codes, scales = torch.empty((128, H), dtype=torch.uint8, device=dev), torch.empty((128, H // 128), device=dev)
+    mx_scales = torch.empty((128, H // 32), dtype=torch.uint8, device=dev)
+    src = torch.randn(128, H, device=dev).to(bf)
+    big = torch.randn(100, H, device=dev).to(bf)
+    calls = [
+        lambda: L.route(x, wr), lambda: L.route(big, wr), lambda: L.permute(idx),
+        lambda: M.moe_route_noalloc(x, wr, None, T, H, E, K, idx, w),
+        lambda: M.moe_quantize_e4m3(src, 128, H, 1, codes, scales),
+        lambda: M.moe_quantize_mx(src, 128, H, 1, codes, mx_scales),
+        lambda: L.combine(torch.zeros(T * K, H, device=dev), inv),
+        lambda: L.dispatch(x, inv), lambda: L.dispatch_bwd(rows, inv), lambda: L.combine_weighted(rows, w, inv),
+        lambda: L.combine_weighted_bwd(x, rows, w, inv), lambda: L.swiglu_ckpt(gu, inv),
+        lambda: L.swiglu_ckpt_bwd(q, s, dh, topk_w=w, inv=inv),
+        lambda: L.route_bwd(x, w, w, offsets, perm_src, perm_k), lambda: L.route_bwd(x, w, w, topk_idx=idx),
+        lambda: L.expert_product(rows, w_gu, offsets), lambda: L.expert_wgrad(gu, rows, offsets),
+    ]
+    failed = []
+    for i, call in enumerate(calls):
+        with pytest.raises(M.MoeError) as e:
+            M.MoeLayer(8192, 8, 2, 8192, n_spare_slots=1000)
+        assert e.value.status == 6
+        try:
+            call()
+        except M.MoeError as err:
+            failed.append((i, str(err)))
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert L.status() == 0
+    L.close()
