@@ -742,9 +742,9 @@ class MoeLayer:
         moe_expert_product(self.ctx, a, w, offsets, P, n_in, n_out, transposed, out, self._stream())
         return out
 
-    def expert_wgrad(self, dy, a, offsets, dtype=torch.bfloat16, out=None, accumulate=False, stream=None):
-        """dw [E, n_out, n_in] = each expert's dy^T a over its rows (dy [P, n_out], a [P, n_in] bf16), bf16 or fp32;
-        with accumulate, added to the fp32 tensor `out`."""
+    def expert_wgrad(self, dy, a, offsets, dtype=None, out=None, accumulate=False, stream=None):
+        """dw [E, n_out, n_in] = each expert's dy^T a over its rows (dy [P, n_out], a [P, n_in] bf16), bf16 or fp32
+        (dtype, or that of `out`; bf16 without either); with accumulate, added to the fp32 tensor `out`."""
         if self._elsewhere(stream):
             with self._on(stream):
                 return self.expert_wgrad(dy, a, offsets, dtype, out, accumulate)
@@ -754,11 +754,17 @@ class MoeLayer:
         _want(a, "a", torch.bfloat16, (P, n_in), self.device)
         _want(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
         if out is not None:
+            if not isinstance(out, torch.Tensor):
+                raise TypeError(f"out: expected a torch.Tensor, got {type(out).__name__}")
+            if dtype is not None and dtype != out.dtype:
+                raise TypeError(f"dtype: {dtype}, but out is {out.dtype}")
             dtype = out.dtype
         elif accumulate:
             raise ValueError("accumulate: needs the tensor to add to (out)")
-        if dtype not in _ROW_TYPES:
-            raise TypeError("dtype: expected bf16 or fp32")
+        elif dtype is None:
+            dtype = torch.bfloat16
+        if dtype not in _ROW_TYPES or (accumulate and dtype != torch.float32):
+            raise TypeError("dtype: expected bf16 or fp32 (fp32 with accumulate)")
         out = self._out(out, "out", dtype, (self.E, n_out, n_in), dy)
         moe_expert_wgrad(self.ctx, dy, a, offsets, P, n_in, n_out, _ROW_TYPES[dtype], accumulate, out, self._stream())
         return out

@@ -41,7 +41,7 @@ from typing import Optional
 
 import torch
 
-from .binding import check_tensor, moe_permute, moe_quantize_e4m3, moe_route, moe_workspace_size
+from .binding import _rows, _want, check_tensor, moe_permute, moe_quantize_e4m3, moe_route, moe_workspace_size
 
 
 @dataclass
@@ -72,6 +72,37 @@ class Grads:
 def _check_weights(layer, w_gu, w_dn):
     check_tensor(w_gu, "w_gu", torch.bfloat16, (layer.E, 2 * layer.I, layer.H), layer.device)
     check_tensor(w_dn, "w_dn", torch.bfloat16, (layer.E, layer.H, layer.I), layer.device)
+
+
+def _check_backward(layer, s, dout, w_router, w_gu, w_dn, w_dtype, into):
+    """All that a call of ``backward`` could refuse, before its first launch: a step that was half done would have added
+    to one of ``into`` and not to the other."""
+    H, E, K, I, d = layer.H, layer.E, layer.K, layer.I, layer.device
+    bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    _check_weights(layer, w_gu, w_dn)
+    T = _rows(dout, "dout")
+    ckpt_x = s.x_scales is not None
+    wanted = [("dout", dout, bf16, (T, H)), ("w_router", w_router, f32, (E, H)),
+              ("saved.x", s.x, u8 if ckpt_x else bf16, (T, H)), ("saved.topk_idx", s.topk_idx, i32, (T, K)),
+              ("saved.topk_w", s.topk_w, f32, (T, K)), ("saved.offsets", s.offsets, i32, (E + 1,)),
+              ("saved.perm_src", s.perm_src, i32, (T * K,)), ("saved.perm_k", s.perm_k, i32, (T * K,)),
+              ("saved.inv", s.inv, i32, (T, K)), ("saved.gu_q", s.gu_q, u8, (T * K, 2 * I)),
+              ("saved.gu_s", s.gu_s, f32, (T * K, 2 * I // 128))]
+    if ckpt_x:
+        wanted.append(("saved.x_scales", s.x_scales, f32, (T, H // 128)))
+    if into is not None:
+        if w_dtype is not None and w_dtype != f32:
+            raise TypeError(f"w_dtype: {w_dtype}, but gradients are added to fp32 tensors")
+        into_gu, into_dn = into
+        wanted += [("into[0]", into_gu, f32, w_gu.shape), ("into[1]", into_dn, f32, w_dn.shape)]
+    elif w_dtype not in (None, bf16, f32):
+        raise TypeError(f"w_dtype: {w_dtype}, expected bf16 or fp32")
+    for name, t, dtype, shape in wanted:
+        _want(t, name, dtype, shape, d)
+    for name, t in (("w_gu", w_gu), ("w_dn", w_dn), ("w_router", w_router), ("dout", dout), ("saved.x", s.x),
+                    ("saved.gu_q", s.gu_q), ("into[0]", into and into[0]), ("into[1]", into and into[1])):
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{name}: must be 16-byte aligned")
 
 
 def _route_and_permute(layer, x, w_router, logit_bias):
@@ -112,14 +143,15 @@ def forward(layer, x, w_router, w_gu, w_dn, logit_bias=None, ckpt_x=False):
     return out, Saved(kept, scales, topk_idx, topk_w, offsets, perm_src, perm_k, inv, gu_q, gu_s)
 
 
-def backward(layer, saved, dout, w_router, w_gu, w_dn, w_dtype=torch.bfloat16, into=None):
+def backward(layer, saved, dout, w_router, w_gu, w_dn, w_dtype=None, into=None):
     """Grads of one step from dout [T, H] bf16 and the forward's Saved.
 
-    The experts' weight gradients come in w_dtype (bf16 or fp32); ``into``, a
-    pair of fp32 tensors (w_gu's, w_dn's), has them added to what it holds
-    (gradient accumulation) and returned instead."""
-    _check_weights(layer, w_gu, w_dn)
+    The experts' weight gradients come in w_dtype (bf16, the default, or fp32);
+    ``into``, a pair of fp32 tensors (w_gu's, w_dn's), has them added to what it
+    holds (gradient accumulation) and returned instead. Arguments are checked
+    before anything is launched or added to."""
     s = saved
+    _check_backward(layer, s, dout, w_router, w_gu, w_dn, w_dtype, into)
     into_gu, into_dn = into if into is not None else (None, None)
     add = into is not None
     with layer._on(None):

@@ -182,6 +182,67 @@ def test_train_step_order_of_calls(host_layer):
         train.forward(L, a["x"], a["wr"], a["w_dn"], a["w_gu"])
 
 
+def test_train_backward_refuses_before_any_call(host_layer):
+    """A backward pass that is refused has launched nothing: a gradient it should add to is never half updated."""
+    from dataclasses import replace
+    from mixture_experts_layer_24_b200 import train
+    L, calls = host_layer
+    a, half, f32 = _args(), torch.float16, torch.float32
+    _, saved = train.forward(L, a["x"], a["wr"], a["w_gu"], a["w_dn"], ckpt_x=True)
+    _, plain = train.forward(L, a["x"], a["wr"], a["w_gu"], a["w_dn"])
+    into = (torch.zeros(a["w_gu"].shape), torch.zeros(a["w_dn"].shape))
+    odd = lambda t: torch.zeros(t.numel() + 1, dtype=t.dtype)[1:].view(t.shape)  # noqa: E731  not 16-byte aligned
+    calls.clear()
+
+    def back(s=saved, dout=a["x"], wr=a["wr"], w_gu=a["w_gu"], w_dn=a["w_dn"], **more):
+        return train.backward(L, s, dout, wr, w_gu, w_dn, **more)
+
+    bad = [
+        lambda: back(into=(into[0][:, :-1], into[1])),
+        lambda: back(into=(into[0].to(torch.bfloat16), into[1])),
+        lambda: back(into=(into[0], into[1].to(torch.bfloat16))),
+        lambda: back(into=(into[0].transpose(1, 2).contiguous().transpose(1, 2), into[1])),
+        lambda: back(into=(odd(into[0]), into[1])),
+        lambda: back(into=(into[1], into[0])),
+        lambda: back(into=(None, into[1])),
+        lambda: back(into=into, w_dtype=torch.bfloat16),
+        lambda: back(w_dtype=half),
+        lambda: back(into=into, dout=a["x"][:-1]),
+        lambda: back(into=into, dout=a["x"].float()),
+        lambda: back(into=into, wr=a["wr"].double()),
+        lambda: back(into=into, wr=odd(a["wr"])),
+        lambda: back(into=into, w_gu=odd(a["w_gu"])),
+        lambda: back(into=into, w_gu=a["w_dn"]),
+        lambda: back(into=into, s=replace(saved, x_scales=None)),
+        lambda: back(into=into, s=replace(saved, topk_w=saved.topk_w[:-1])),
+        lambda: back(into=into, s=replace(plain, perm_k=plain.perm_k.long())),
+        lambda: back(into=into, s=replace(saved, gu_q=saved.gu_q[:, :-1])),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+        assert not calls, f"bad call {i} reached the C ABI"
+    for s in (saved, plain):
+        g = back(s=s, into=into, w_dtype=f32)
+        assert g.w_gu is into[0] and g.w_dn is into[1]
+        assert back(s=s, into=into).w_gu is into[0]
+        assert back(s=s).w_gu.dtype == torch.bfloat16 and back(s=s, w_dtype=f32).w_dn.dtype == f32
+
+
+def test_weight_gradient_of_another_type_than_its_output_is_refused(host_layer):
+    L, calls = host_layer
+    a, f32, bf16 = _args(), torch.float32, torch.bfloat16
+    out = torch.zeros((8, 256, 256))
+    for kw in (dict(dtype=bf16, out=out), dict(dtype=f32, out=out.to(bf16)), dict(out=out.to(bf16), accumulate=True),
+               dict(out=out.double()), dict(out=[0])):
+        with pytest.raises((TypeError, ValueError)):
+            L.expert_wgrad(a["gu"], a["rows"], a["offsets"], **kw)
+    assert not calls
+    assert L.expert_wgrad(a["gu"], a["rows"], a["offsets"]).dtype == bf16
+    assert L.expert_wgrad(a["gu"], a["rows"], a["offsets"], out=out) is out
+    assert L.expert_wgrad(a["gu"], a["rows"], a["offsets"], dtype=f32, out=out, accumulate=True) is out
+
+
 def _difference(f, v, i, step=1e-6):
     """Central difference of f at flat place i of v (float64: error about step^2 + eps/step, 1e-10 of f's scale)."""
     keep = v.reshape(-1)[i].item()
