@@ -206,6 +206,41 @@ def test_swiglu_ckpt_infinities_and_nan(layers):
     assert torch.isfinite(h[5]).all()
 
 
+def test_swiglu_nan_and_infinity_places(layers):
+    """h, dgu, hw and the weights' gradient hold NaN and infinities exactly where the formulas in fp32 do, and nowhere
+    else: values that reach no overflow of their own (|g| < 80), beside infinities and NaN in g, u and dh."""
+    rows, I = 24, 256
+    L = layers(128, 8, 1, I)
+    gu, dh = _rand(160, rows, 2 * I, std=2.0), _rand(161, rows, I)
+    inf, nan = float("inf"), float("nan")
+    for i, (col, v) in enumerate(((3, inf), (I + 5, inf), (7, nan), (I + 130, nan), (9, -inf), (I + 9, -inf))):
+        gu[i, col] = v
+    gu[6, 11], gu[6, I + 11] = inf, nan
+    gu[7, 12], gu[7, I + 12] = -inf, 0.0
+    gu[8, 13], gu[8, I + 13] = inf, 0.0
+    h, q, s = L.swiglu_ckpt(gu)
+    g, u = gu[:, :I].float(), gu[:, I:].float()
+    ref = g / (1 + torch.exp(-g)) * u
+    assert torch.equal(torch.isnan(h), torch.isnan(ref))
+    assert torch.equal(torch.isinf(h), torch.isinf(ref))
+    assert torch.equal(torch.signbit(h)[torch.isinf(h)], torch.signbit(ref)[torch.isinf(h)])
+    # the gradient from a checkpoint without them, and dh with them
+    clean = _rand(162, rows, 2 * I, std=2.0)
+    _, q, s = L.swiglu_ckpt(clean)
+    dh[0, 3], dh[1, I - 1], dh[2, 0] = inf, -inf, nan
+    w = torch.rand(rows, 1, device="cuda") + 0.5
+    w[3] = 0.0
+    w[4], w[5] = inf, nan
+    inv = torch.arange(rows, dtype=torch.int32, device="cuda").view(-1, 1)
+    dgu, hw, dw = L.swiglu_ckpt_bwd(q, s, dh, topk_w=w, inv=inv)
+    v = R.decode(q, s)
+    dg, du, h64, dots = R.swiglu_bwd(v[:, :I], v[:, I:], dh.to(F64), w.view(-1).to(F64))
+    for got, want in ((dgu[:, :I], dg), (dgu[:, I:], du), (hw, w.to(F64) * h64), (dw.view(-1), dots)):
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.isinf(got), torch.isinf(want))
+    assert L.status() == 0
+
+
 @pytest.mark.parametrize("T,K,I,drop", ACT)
 @pytest.mark.parametrize("weighted", [False, True])
 def test_swiglu_ckpt_bwd(layers, T, K, I, drop, weighted):
