@@ -281,6 +281,33 @@ def test_swiglu_ckpt_bwd(layers, T, K, I, drop, weighted):
     assert (dw[~kept] == 0).all()
 
 
+def test_swiglu_codes_over_all_pairs_of_values(layers):
+    """The codes' short cut (a reciprocal per block and a correction in place of a division per code) over every block
+    maximum a bf16 can hold and every value up to it, signs mixed: the block quantiser's bits, which divides."""
+    import mixture_experts_layer_24_b200 as M
+    I, per = 8192, 127  # values beside the maximum in a block of 128
+    L = layers(128, 8, 1, I)
+    top = 0x7f80  # bit patterns of positive finite bf16 values lie below infinity's
+    blocks = torch.arange((top + per - 1) // per, device="cuda")
+    checked = 0
+    for first in range(1, top, 256):
+        amax = torch.arange(first, min(first + 256, top), device="cuda")
+        bits = (blocks[:, None] * per + torch.arange(per, device="cuda")).view(1, -1, per)
+        bits = torch.minimum(bits.expand(len(amax), -1, -1), amax[:, None, None])
+        keep = (blocks * per)[None, :] <= amax[:, None]  # blocks that hold a value up to the maximum
+        vals = torch.cat((bits, amax[:, None, None].expand(-1, len(blocks), 1)), 2)[keep]
+        vals = (vals + (torch.arange(128, device="cuda") % 3 == 1) * 0x8000).to(torch.int32)
+        vals = torch.where(vals >= 0x8000, vals - 0x10000, vals).to(torch.int16)
+        pad = -vals.shape[0] % (2 * I // 128)
+        gu = torch.cat((vals, vals[:1].expand(pad, -1))).view(BF16).view(-1, 2 * I).contiguous()
+        _, q, s = L.swiglu_ckpt(gu)
+        q2, s2 = torch.empty_like(q), torch.empty_like(s)
+        M.moe_quantize_e4m3(gu, gu.shape[0], 2 * I, 1, q2, s2)
+        assert torch.equal(q, q2) and torch.equal(s, s2), first
+        checked += vals.shape[0] * per
+    assert checked >= top * (top - 1) // 2 and L.status() == 0
+
+
 @pytest.mark.parametrize("I", [128, 640, 2048, 8192])
 def test_swiglu_rows_do_not_depend_on_each_other(layers, I):
     """A pair's codes, gradients and weight's gradient have the same bits alone, among few and among many."""
