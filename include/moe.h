@@ -120,7 +120,9 @@ moe_status_t moe_ctx_destroy(moe_ctx_t* ctx);
 
 /* Bytes of workspace moe_forward / moe_expert_ffn / moe_route / moe_permute
  * need for T tokens. The caller allocates it on the context's device
- * (256-byte aligned) and may reuse it between calls on the same stream. */
+ * (256-byte aligned) and may reuse it between calls on the same stream. Calls
+ * that may overlap (several streams or threads, graphs replayed beside each
+ * other) need workspaces of their own; they may share the context. */
 size_t moe_workspace_size(const moe_ctx_t* ctx, int T);
 
 /* Router: logits in the fixed order below, top-k, renormalised weights.

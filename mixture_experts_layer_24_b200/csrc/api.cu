@@ -616,13 +616,13 @@ moe_status_t moe_ctx_create(moe_ctx_t** out, const moe_config_t* cfg) {
   ctx->chain = !(cfg->flags & MOE_FLAG_NO_PDL);
   ctx->encode = reinterpret_cast<EncodeTiledFn>(fn);
   if (lib_malloc(&ctx->d_status, sizeof(int)) != cudaSuccess ||
-      lib_malloc(&ctx->d_counters, sizeof(unsigned int) * kRouteSmallMaxT) != cudaSuccess) {
+      lib_malloc(&ctx->d_counters, sizeof(unsigned int) * kRouteCounters) != cudaSuccess) {
     cudaFree(ctx->d_status);
     delete ctx;
     return fail(MOE_ERR_OOM, "cudaMalloc of the context's device words failed");
   }
   cudaMemset(ctx->d_status, 0, sizeof(int));
-  cudaMemset(ctx->d_counters, 0, sizeof(unsigned int) * kRouteSmallMaxT);
+  cudaMemset(ctx->d_counters, 0, sizeof(unsigned int) * kRouteCounters);
   cudaDeviceSynchronize();
   *out = ctx;
   return MOE_OK;
@@ -720,8 +720,8 @@ moe_status_t route_impl(moe_ctx_t* ctx, const void* x, const float* w_router, co
   if (T <= kRouteSmallMaxT) {
     Prof p(ctx, MOE_PROF_ROUTER, s);
     MOE_CUDA(launch_route_small(x, w_router, logit_bias, T, c.hidden, c.n_experts, c.top_k, logits, topk_idx,
-                                topk_w, ctx->d_counters, ctx->d_status, s, ctx->chain, sched, sched_n, rd, map_of,
-                                planned));
+                                topk_w, T <= 4 ? ctx->route_counter(s) : nullptr, ctx->d_status, s, ctx->chain, sched,
+                                sched_n, rd, map_of, planned));
     return MOE_OK;
   }
   {

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <mutex>
 #include <string>
+#include <unordered_map>
 #include <vector>
 
 #include "../../include/moe.h"
@@ -25,13 +26,18 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+constexpr int kRouteCounters = 4096;
+
 struct moe_ctx {
   moe_config_t cfg;
   int device = 0;
   int* d_status = nullptr;
   int num_sms = 148;
   bool chain = true;  // programmatic dependent launch between this library's kernels
-  unsigned int* d_counters = nullptr;  // arrival counters of the decode router (self-resetting)
+  unsigned int* d_counters = nullptr;  // [kRouteCounters] arrival counters of the decode router (self-resetting)
+  std::mutex counters_mu;
+  int counters_taken = 0;
+  std::unordered_map<unsigned long long, int> counter_of_stream;
   int host_status = 0;
   EncodeTiledFn encode = nullptr;
   std::atomic<int64_t> launches{0};
@@ -46,6 +52,27 @@ struct moe_ctx {
   double prof_ms[MOE_PROF_KINDS] = {};
   int64_t prof_n[MOE_PROF_KINDS] = {};
   std::mutex prof_mu;
+
+  // The arrival counter of a decode router launch on s, shared with no launch that may run beside it: launches on one
+  // stream follow each other and take the stream's; a captured launch keeps one for good, since its graph may be
+  // replayed beside anything (but not beside itself). NULL when all are taken.
+  unsigned int* route_counter(cudaStream_t s) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
+        (capture == cudaStreamCaptureStatusNone && cudaStreamGetId(s, &id) != cudaSuccess)) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    std::lock_guard<std::mutex> g(counters_mu);
+    if (capture == cudaStreamCaptureStatusNone) {
+      const auto it = counter_of_stream.find(id);
+      if (it != counter_of_stream.end()) return d_counters + it->second;
+    }
+    if (counters_taken == kRouteCounters) return nullptr;
+    if (capture == cudaStreamCaptureStatusNone) counter_of_stream[id] = counters_taken;
+    return d_counters + counters_taken++;
+  }
 
   // cuTensorMapEncodeTiled on the current device. It is a driver call and needs that device's context current on this
   // thread; a thread whose first CUDA call this is has none yet (cudaGetDevice binds nothing, cudaSetDevice does).

@@ -483,8 +483,7 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_small_kernel(const uint16
 template <int TG>
 static cudaError_t launch_rs(const void* x, const float* wr, const float* bias, int T, int H, int E, int K,
                              float* logits, int32_t* idx, float* w, unsigned int* counters, int fuse, int* status,
-                             cudaStream_t s, int* sched, int sched_n, const ResidencyDev* rd = nullptr,
-                             int32_t* map_of = nullptr) {
+                             cudaStream_t s, int* sched, int sched_n, const ResidencyDev* rd, int32_t* map_of) {
   const size_t smem = route_small_smem(TG, H);
   // One limit for every call: another thread could lower that of this call's H before the launch below.
   cudaError_t err = cudaFuncSetAttribute(route_small_kernel<TG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -504,7 +503,7 @@ static cudaError_t launch_rs(const void* x, const float* wr, const float* bias, 
 // 64 tokens. Rows that a bulk copy cannot take (not 16-byte aligned, or too
 // large for shared memory) go through the direct kernel.
 cudaError_t launch_route_small(const void* x, const float* wr, const float* bias, int T, int H, int E, int K,
-                               float* logits, int32_t* idx, float* w, unsigned int* counters, int* status,
+                               float* logits, int32_t* idx, float* w, unsigned int* counter, int* status,
                                cudaStream_t s, bool pdl, int* sched, int sched_n, const ResidencyDev* rd,
                                int32_t* map_of, bool* planned) {
   if (planned) *planned = false;
@@ -517,18 +516,16 @@ cudaError_t launch_route_small(const void* x, const float* wr, const float* bias
     if (err != cudaSuccess) return err;
     return launch_topk_warp(logits, T, E, K, idx, w, s, false);
   }
-  // the fused last CTA runs the residency plan when the caller asks for it (and learns it through *planned)
-  const ResidencyDev* rdp = (T <= 4 && planned) ? rd : nullptr;
-  if (rdp) *planned = true;
-  if (T <= 1)
-    return launch_rs<1>(x, wr, bias, T, H, E, K, logits, idx, w, counters, 1, status, s, sched, sched_n, rdp, map_of);
-  if (T <= 2)
-    return launch_rs<2>(x, wr, bias, T, H, E, K, logits, idx, w, counters, 1, status, s, sched, sched_n, rdp, map_of);
-  if (T <= 4)
-    return launch_rs<4>(x, wr, bias, T, H, E, K, logits, idx, w, counters, 1, status, s, sched, sched_n, rdp, map_of);
+  if (T <= 4 && counter) {
+    // the fused last CTA runs the residency plan when the caller asks for it (and learns it through *planned)
+    const ResidencyDev* rdp = planned ? rd : nullptr;
+    if (rdp) *planned = true;
+    auto* launch = T <= 1 ? launch_rs<1> : T <= 2 ? launch_rs<2> : launch_rs<4>;
+    return launch(x, wr, bias, T, H, E, K, logits, idx, w, counter, 1, status, s, sched, sched_n, rdp, map_of);
+  }
   if (T <= 8) {
-    const cudaError_t err = launch_rs<8>(x, wr, bias, T, H, E, K, logits, idx, w, counters, 0, status, s, sched,
-                                         sched_n);
+    const cudaError_t err = launch_rs<8>(x, wr, bias, T, H, E, K, logits, idx, w, nullptr, 0, status, s, sched, sched_n,
+                                         nullptr, nullptr);
     if (err != cudaSuccess) return err;
     return launch_topk_warp(logits, T, E, K, idx, w, s, pdl);
   }
