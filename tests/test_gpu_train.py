@@ -838,6 +838,25 @@ def test_activation_and_products_past_32_bit_offsets(layers):
     assert L.status() == 0
 
 
+def test_router_gradient_of_the_most_pairs(layers):
+    """65536 tokens of 32 pairs, half of them of one expert or its neighbour, from a list and from the choice."""
+    T, K, E, H = 65536, 32, 64, 128
+    L, r = layers(H, E, K), _cuda(R.routing(T, K, E, 170, drop=0.02, skew=3.0))
+    x, dw = _rand(171, T, H), _rand(172, T, K, dtype=F32)
+    listed = L.route_bwd(x, r["w"], dw, r["offsets"], r["perm_src"], r["perm_k"])
+    chosen = L.route_bwd(x, r["w"], dw, topk_idx=r["idx"])
+    for got, inv in ((listed, r["inv"]), (chosen, torch.zeros_like(r["inv"]))):
+        dl_ref, dwr_ref, db_ref, dl_mag, dwr_mag, db_mag = R.route_bwd(x, r["w"], dw, r["idx"], inv, E)
+        _within(got[0], dl_ref, (K + 2) * U * dl_mag * 1.01, "dlogit")
+        most = T  # an expert's pairs: every token at most
+        _within(got[1], dwr_ref, (K + 4 + most) * U * dwr_mag * 1.01, "dw_router")
+        _within(got[2], db_ref, (K + 3 + most) * U * db_mag * 1.01, "dlogit_bias")
+        # the sums are split over many blocks, so the error is far below that bound: 2-norm within 2^-20
+        for a, b in ((got[1], dwr_ref), (got[2], db_ref)):
+            assert (a.to(F64) - b).norm() <= 2.0 ** -20 * b.norm()
+    assert L.status() == 0
+
+
 def test_router_gradient_in_plain_stream_order(layers):
     """Without programmatic dependent launch: the same bits."""
     import mixture_experts_layer_24_b200 as M
