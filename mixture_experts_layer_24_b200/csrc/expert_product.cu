@@ -63,9 +63,10 @@
 // it costs), eight epilogue warps (no faster), 32-byte stores straight from the
 // lanes (to 30% slower with few rows per expert), coalesced stores from shared
 // memory instead of TMA stores and eviction hints on those (no faster), nine
-// smaller steps in flight for few rows (no faster). The weights' gradient is
-// held up by its writes: 12 experts x 683 rows in fp32 take 289 us, 209 without
-// the stores, 196 without the epilogue (tensor pipe 53% busy; forward 90%).
+// smaller steps in flight for few rows (no faster). The fp32 weights' gradient
+// is slower for its stores: 12 experts x 683 rows take 289 us, 209 without
+// them, 196 without the epilogue (tensor pipe 53% busy, DRAM 2.8 TB/s; forward
+// 90%). Where a store waits (DRAM, the L2 port, the staging boxes) is not known.
 #include <algorithm>
 
 #include "common.cuh"
@@ -80,22 +81,22 @@ constexpr int kTileN = 256;
 // K steps in flight: the weights' gradient gives one up for its tails and a third store box per warp.
 __host__ __device__ constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
 // N tiles of an expert that are in flight together, against all of its M tiles in turn: with all N tiles innermost,
-// one expert of 32768 rows re-read its rows from HBM for every M tile (then 1166 us under the power cap, 879 us in bands
-// of 8, 864 in bands of 4; the weights' gradient is 1% faster in bands of 8).
+// one expert of 32768 rows re-read its rows from HBM for every M tile (then 1166 us under the power cap, 879 us in
+// bands of 8, 864 in bands of 4; the weights' gradient is 1% faster in bands of 8).
 constexpr int kBand = 8;
 constexpr uint32_t kOpBytes = 128 * 128;          // one operand's half tile: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOpBytes;    // [M operand][N operand]
 constexpr int kThreads = 224;
 __host__ __device__ constexpr int barriers(bool wgrad) { return 2 * stages(wgrad) + 10; }
-// K steps summed in TMEM before an fp32 gradient goes out. Over 16384 rows in one run it was 1.9e-5 off (2-norm, terms of
-// both signs), over 65536 rows 7.6e-5. In segments of 14 steps (896 rows) the error does not grow with the rows: 6.5e-7
-// (terms of both signs), or 1.5e-6 low (positive terms), where fp32 multiply-adds have 1.9e-7. Time at 8192 rows,
-// 4096 x 4096: 238 us in one run, 252 us in segments of 32 steps, 272 us of 16, 286 us of 14, 326 us of 8.
+// K steps summed in TMEM before an fp32 gradient goes out. Over 16384 rows in one run it was 1.9e-5 off (2-norm, terms
+// of both signs), over 65536 rows 7.6e-5. In segments of 14 steps (896 rows) the error does not grow with the rows:
+// 6.5e-7 (terms of both signs), or 1.5e-6 low (positive terms), where fp32 multiply-adds have 1.9e-7. Time at 8192
+// rows, 4096 x 4096: 238 us in one run, 252 us in segments of 32 steps, 272 us of 16, 286 us of 14, 326 us of 8.
 constexpr int kSegment = 14;
 // K steps of one run of a bf16 gradient (32768 rows). Without it, positive terms over 65536 rows came out 6.5e-4 low,
 // over 524288 rows 3.2e-3, over 2097152 rows 1.2e-2. The sum of the runs so far stays in one accumulator while the
-// other takes the next run; the MMA waits while the epilogue adds it (one expert of 131072 rows, 4096 x 4096: within the
-// noise of one run's time). Experts of up to 32768 rows are summed as before it.
+// other takes the next run; the MMA waits while the epilogue adds it (one expert of 131072 rows, 4096 x 4096: 3590 us,
+// 3660 us in one run, within each other's noise). Experts of up to 32768 rows are one run.
 constexpr int kLongRun = 512;
 constexpr uint32_t kBoxBytes = 64 * 128;          // MN-major box: 64 K rows x 64 elements
 constexpr uint32_t kStoreBox = 32 * 128;          // one warp's store box: 32 rows x 128 bytes

@@ -22,12 +22,15 @@
 // the pieces write dl out for every pair, dropped ones too.
 //
 // x is read from L2 once per pair (K times over), 268 MB for 4096 tokens of
-// 8 x 4096: 31.5 us for the two kernels, where HBM needs 6.2 us for x and dWr
-// once. What bounds it is issue and latency together: paired fp32 multiply-adds
-// (one instruction, two columns) and four rows in flight, four blocks per SM
-// (three or five: 37 and 44 us); 16 columns per thread took 36 us, eight rows
-// in flight 42 us, rows through shared memory by asynchronous copies 54 us, and
-// a single thread's walk over the longest expert's parts 4 us more.
+// 8 x 4096: 31.5 us for the two kernels on warm inputs, 35 to 37 us a call on
+// new ones, where HBM needs 6.2 us for x and dWr once. What bounds it is issue
+// and latency together: paired fp32 multiply-adds (one instruction, two
+// columns) and four rows in flight, four blocks per SM (three or five: 37 and
+// 44 us); 16 columns per thread took 36 us, eight rows in flight 42 us, rows
+// through shared memory by asynchronous copies, once per pair as here, 54 us,
+// and a single thread's walk over the longest expert's parts 4 us more. A block
+// that keeps a few columns of all tokens in shared memory would read x once and
+// have no parts to join; it has not been built.
 #include <algorithm>
 #include <type_traits>
 
@@ -252,10 +255,13 @@ __global__ void __launch_bounds__(256) route_wgrad_join_kernel(const int32_t* __
   if (dbias && blockIdx.y == 0 && threadIdx.x == 0) dbias[e] = bias;
 }
 
-// Pairs per piece: two pieces per SM (at 32768 pairs of 384 experts three cost 2 us more, four 3 us: more parts to
-// add), 8 at least (a CTA's serial walk is the time then) and 128 at most.
+// Pairs per piece: two pieces per SM of a B200 (at 32768 pairs of 384 experts three cost 2 us more, four 3 us: more
+// parts to add), 8 at least (a CTA's serial walk is the time then) and 128 at most. The number of SMs is a constant,
+// so that the order of the sums follows from the number of pairs alone, on a part of a GPU too.
+constexpr int kPieces = 2 * 148;
+
 int route_bwd_chunk(int P) {
-  const int c = (P + 2 * 148 - 1) / (2 * 148);
+  const int c = (P + kPieces - 1) / kPieces;
   return std::min(kChunkMax, std::max(8, (c + 3) / 4 * 4));
 }
 

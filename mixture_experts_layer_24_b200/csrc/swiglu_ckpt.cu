@@ -17,15 +17,21 @@
 //
 // Bound by HBM: 8 bytes and 10 bytes per (row, column of I). Measured at 32768
 // rows, I = 2048, of a copy's 6.56 TB/s: forward 91.7 us (90%), gradient with
-// weights 115 us (89%). What stood in the way was arithmetic: with IEEE
-// divisions (one per code, one per sigmoid) and 8 lanes' worth of shuffles the
-// forward took 166 us. Codes now take a reciprocal per block and three fused
-// multiply-adds per value, to the same bits (below); the sigmoid takes the fast
-// exponential and division, whose error (at most (2 + 1.2 |g|) 2^-23, and
-// 2^-22) is far below the bf16 rounding that follows; a block's amax is taken
-// in bf16, two values at a time, over 8 lanes of 16 values (16 lanes of 8
+// weights 115 us (89%) on warm inputs; on new ones 97 and 121 us a call (84 and
+// 85%). What stood in the way was arithmetic: with IEEE divisions (one per
+// code, one per sigmoid) and 8 lanes' worth of shuffles the forward took 166
+// us. Codes now take a reciprocal per block and three fused multiply-adds per
+// value, to the same bits (below). The sigmoid takes the fast exponential and
+// division, whose relative error is at most (2 + 1.2 |g|) 2^-23 and 2^-22: far
+// below the bf16 rounding that follows in h, dgu and hw. dw is not rounded to
+// bf16, and keeps fp32's accuracy all the same: of the sum of its terms'
+// magnitudes over 2048 columns at most 2.2e-8 off (expf and torch's fp32 sum:
+// 2.1e-8), with every g near -20 1.5e-7 (1.0e-7), near -80 6.8e-7 (3.5e-7);
+// expf in its place took the gradient from 117 to 123 us. A block's amax is
+// taken in bf16, two values at a time, over 8 lanes of 16 values (16 lanes of 8
 // values: 109 us). The register bounds are those measured fastest: forward 48
-// (58 unbounded: 101 us), gradient 64 (74 unbounded: 121 us).
+// (58 unbounded: 101 us), gradient 64 (74 unbounded: 121 us, where the bounded
+// one took 115).
 #include "rows.cuh"
 #include "train.h"
 
@@ -55,7 +61,8 @@ __device__ __forceinline__ float2 block_amax(const uint4 (&g)[2], const uint4 (&
 }
 
 // v / s rounded to nearest, as IEEE division rounds it, for a bf16 v with |v| <= amax, s = RN(amax / 448) and r the
-// fast reciprocal of s: one correction of v * r by its exact remainder.
+// fast reciprocal of s: one correction of v * r by its exact remainder, the step of Newton's method for the quotient
+// that a fused multiply-add allows (Markstein's).
 __device__ __forceinline__ float quotient(float v, float s, float r) {
   const float y = v * r;
   return fmaf(fmaf(-s, y, v), r, y);

@@ -23,8 +23,9 @@ cudaError_t launch_swiglu_ckpt_bwd(const uint8_t* q, const float* s, const void*
 size_t route_bwd_workspace_floats(int P, int H);
 constexpr int kRouteBwdLaunches = 2;
 cudaError_t launch_route_bwd(const void* x, const float* scales, const float* w, const float* dw,
-                             const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T, int K, int E, int H, float* dl,
-                             float* dwr, float* dbias, float* ws, int* status, cudaStream_t s, bool pdl);
+                             const int32_t* offsets, const int32_t* perm_src, const int32_t* perm_k, int T, int K,
+                             int E, int H, float* dl, float* dwr, float* dbias, float* ws, int* status, cudaStream_t s,
+                             bool pdl);
 
 // Tensor maps of one expert product: the M operand (weights, or dy), the N
 // operand (rows) and the output of the weights' gradient. A K-major N operand

@@ -45,7 +45,7 @@ constexpr unsigned kSlice = 64;
 enum Sum { kPlain, kWeighted, kRouter };
 
 // One thread per 16-byte piece of the output row.
-template <class R, bool kCkpt>
+template <bool kCkpt>
 __global__ void __launch_bounds__(256) dispatch_kernel(const void* __restrict__ x, const float* __restrict__ scales,
                                                         const int32_t* __restrict__ inv, int T, int K, unsigned V,
                                                         uint4* __restrict__ xs, int* status) {
@@ -134,9 +134,10 @@ __device__ __forceinline__ void add_router(float (&acc)[kN], float d, const floa
 
 // kWeighted: out = sum_k w y (the combine). Otherwise the dispatch's gradient, kRouter: with the router's term.
 //
-// Router rows are fp32: where expert rows are bf16, a thread takes columns 4l..4l+3 of both halves of a 128-column block
-// in place of eight neighbouring ones, so that a warp's loads of router rows are contiguous too (77.7 -> 73.3 us for
-// 4096 tokens of 8 x 4096; slices and one router row at a time, which lets six blocks fit an SM: 67.7 us).
+// Router rows are fp32: where expert rows are bf16, a thread takes columns 4l..4l+3 of both halves of a 128-column
+// block in place of eight neighbouring ones, so that a warp's loads of router rows are contiguous too (77.7 -> 73.3 us
+// for 4096 tokens of 8 x 4096; slices and one router row at a time, which lets six blocks fit an SM: 67.7 us). Slices
+// narrower than 512 columns were not measured.
 template <class R, Sum kSum>
 __global__ void __launch_bounds__(256, kSum == kRouter && R::kN == 8 ? 6 : 5)
     gather_sum_kernel(const uint4* __restrict__ rows, const float* __restrict__ w, const int32_t* __restrict__ inv,
@@ -255,9 +256,9 @@ cudaError_t launch_dispatch(const void* x, const float* scales, int dtype, const
   const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
   const unsigned blocks = blocks_for((long long)T * V);
   if (dtype == MOE_T_E4M3_B128)
-    dispatch_kernel<RowBf16, true><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
+    dispatch_kernel<true><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
   else
-    dispatch_kernel<RowBf16, false><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
+    dispatch_kernel<false><<<blocks, 256, 0, s>>>(x, scales, inv, T, K, V, o, status);
   return cudaGetLastError();
 }
 
@@ -280,11 +281,8 @@ cudaError_t launch_combine_weighted(const void* y, int dtype, const float* w, co
   uint4* o = static_cast<uint4*>(out);
   const unsigned V = (unsigned)(dtype == MOE_T_F32 ? H / 4 : H / 8);
   const unsigned blocks = blocks_for((long long)T * V);
-  if (dtype == MOE_T_F32)
-    gather_sum_kernel<RowF32, kWeighted><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o, status);
-  else
-    gather_sum_kernel<RowBf16, kWeighted><<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o,
-                                                            status);
+  auto sum = dtype == MOE_T_F32 ? gather_sum_kernel<RowF32, kWeighted> : gather_sum_kernel<RowBf16, kWeighted>;
+  sum<<<blocks, 256, 0, s>>>(r, w, inv, nullptr, nullptr, nullptr, T, K, 0, V, o, status);
   return cudaGetLastError();
 }
 
