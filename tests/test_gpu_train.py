@@ -126,6 +126,34 @@ def test_combine_weighted_and_its_gradient(layers, T, K, E, H, drop, gone, dtype
     assert (dw[~kept] == 0).all() and (dy[r["n"]:] == 7).all() and L.status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_at_the_widest(layers, dtype):
+    """H = 8192 through every row operator, against its 64-bit form."""
+    T, K, E, H = 61, 5, 33, 8192
+    L, r = layers(H, E, K), _cuda(R.routing(T, K, E, 21, 0.1, 60))
+    rows, x = _poison_behind(_rand(185, T * K, H, dtype=dtype), r["n"]), _rand(186, T, H, dtype=dtype)
+    xs = L.dispatch(x, r["inv"])
+    assert torch.equal(xs[:r["n"]], x[r["perm_src"][:r["n"]].long()])
+    for more in ((), (_rand(187, T, K, dtype=F32), r["idx"], _rand(188, E, H, dtype=F32))):
+        ref, mag = R.dispatch_bwd(rows, r["inv"], *more)
+        _within(L.dispatch_bwd(rows, r["inv"], *more), ref,
+                2 * K * U * mag * 1.01 + R.half(dtype) * ref.abs() * 1.01, "dx")
+    ref, mag = R.combine(rows, r["w"], r["inv"])
+    bound = K * U * mag * 1.01 + R.half(dtype) * ref.abs() * 1.01
+    _within(L.combine_weighted(rows, r["w"], r["inv"]), ref, bound, "out")
+    dy, dw = L.combine_weighted_bwd(x, rows, r["w"], r["inv"])
+    want, dw_ref, dw_mag = R.combine_bwd(x, rows, r["w"], r["inv"])
+    kept = r["inv"] >= 0
+    _within(dy[r["inv"][kept].long()], want[kept], want[kept].abs() * (R.half(dtype) + 2 * U), "dy")
+    _within(dw, dw_ref, (H + 1) * U * dw_mag * 1.01, "dw")
+    if dtype == BF16:
+        up = _rand(189, T, K, dtype=F32)
+        got = L.route_bwd(x, r["w"], up, topk_idx=r["idx"])
+        ref = R.route_bwd(x, r["w"], up, r["idx"], torch.zeros_like(r["inv"]), E)
+        _within(got[1], ref[1], (K + 4 + T) * U * ref[4] * 1.01, "dw_router")
+    assert L.status() == 0
+
+
 def test_combine_gradient_against_differences(layers):
     """fp32 rows: <out, dout> is linear in each weight and each row, so a difference with step 1 is the gradient up
     to the forward's own rounding."""
@@ -573,6 +601,31 @@ def test_wgrad_fp32_over_many_rows(layers):
     _within(base, ref + 1, (56 + 19 + 2) * 2.0 ** -23 * (mag + 1), "accumulated dw")
     half = L.expert_wgrad(dy, a, off)  # bf16: one run, one rounding
     _within(half, ref, (1024 * 2.0 ** -23 + R.BF16_HALF) * mag * 1.01, "bf16 dw")
+
+
+@pytest.mark.parametrize("n_in,n_out", [(16384, 2432), (2432, 16384), (16384, 16256)])
+def test_products_at_the_widest(layers, n_in, n_out):
+    """The most features, in an odd number of tiles and of bands, over whole numbers: every bit is pinned."""
+    counts = [70, 0, 300]
+    L, (off, P) = layers(256, 3, 1, 128), _segments(counts, 3)
+    n = P - 3
+    w = _ints(180, 3, n_out, n_in)
+    a, dy = _ints(181, P, n_in), _ints(182, P, n_out)
+    _poison_behind(a, n)
+    _poison_behind(dy, n)
+    cut = off.tolist()
+    for rows, transposed in ((a, False), (dy, True)):
+        out = torch.full((P, n_in if transposed else n_out), 7.0, dtype=BF16, device="cuda")
+        L.expert_product(rows, w, off, transposed=transposed, out=out)
+        for e, (i, j) in enumerate(zip(cut, cut[1:])):
+            m = w[e] if transposed else w[e].t()
+            assert torch.equal(out[i:j], (rows[i:j].to(F64) @ m.to(F64)).to(F32).to(BF16))
+        assert (out[n:] == 7).all()
+    for dtype in (BF16, F32):
+        dw = L.expert_wgrad(dy, a, off, dtype=dtype)
+        for e, (i, j) in enumerate(zip(cut, cut[1:])):
+            assert torch.equal(dw[e], (dy[i:j].to(F64).t() @ a[i:j].to(F64)).to(F32).to(dtype))
+    assert L.status() == 0
 
 
 def test_wgrad_bf16_over_the_most_rows(layers):
