@@ -95,7 +95,8 @@ moe_status_t check_route_bwd(const moe_ctx_t* ctx, const void* x, const float* t
   if (T > 0 && (!x || !topk_w || !dtopk_w || !dlogit)) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
   if (!aligned16({x, dw_router})) return fail(MOE_ERR_INVALID_ARG, "x and dw_router must be 16-byte aligned");
   if (need && (!ws || ws_bytes < need))
-    return fail(MOE_ERR_INVALID_ARG, "workspace too small (see moe_route_bwd_workspace_size)");
+    return fail(MOE_ERR_INVALID_ARG,
+                "workspace too small (see moe_route_bwd_workspace_size, moe_route_bwd_topk_workspace_size)");
   if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   return MOE_OK;
 }
